@@ -342,6 +342,75 @@ int kvq_dequantize(const kvq_layout* layout, const kvq_cache* cache,
                    const int32_t* lens, int max_len, float* k_out, float* v_out,
                    kvq_stream_t stream);
 
+/* Attention with sinks and a sliding span (two forms below): a query at
+ * position t attends to the cached positions x <= t with
+ *     x < sinks  or  t - x < span
+ * that is, to the first `sinks` positions of its sequence and to the newest
+ * `span` positions up to its own; s = sm_scale * q K^T over them, a =
+ * softmax(s), o = a V as in kvq_decode_attention (page keys of rotated
+ * layouts are scored with the rotated query, ring keys with the plain one).
+ * Not in the pages: it bounds the cost of a token and, since pages that no
+ * later query sees may be released, the memory of a sequence.
+ *  - A position whose page is absent (page-table entry outside [0,
+ *    num_pages)) is not attended to and not read.  A page may be released
+ *    (its entry set to -1, the page reused) once all its positions are >=
+ *    sinks and more than span - 1 behind every query still to come.
+ *  - sinks, span >= 0; span = INT_MAX sees every position, span = 0 only
+ *    the sinks.  A query that sees nothing gets out = 0, lse = -inf.
+ *  - Every layout that the library accepts; `span` is independent of
+ *    layout->window (what the bf16 ring holds).
+ *  - q is KVQ_BF16 or KVQ_F32, its rows [Hq][d] start q_stride elements
+ *    apart: at least Hq*d, a multiple of 16 bytes (the query columns of a
+ *    joint projection can be passed as they lie); q 16-byte aligned.
+ *  - out is bf16, rows [Hq][d] without gaps, 16-byte aligned; lse fp32 rows
+ *    [Hq] (natural log) or NULL.
+ *  - Scores, softmax statistics and sums are fp32; attention weights and
+ *    reconstructed keys and values are rounded to fp16 at the tensor cores,
+ *    so reconstructed values must lie within +-65504.  out is within 1e-3 +
+ *    1e-3*|o| + bf16 rounding of the same sum in fp64, lse within 1e-3 +
+ *    1e-3*|lse|, for normal inputs (rows of unit-scale scores).
+ *  - No workspace; calls on different streams may overlap as long as no
+ *    call writes the cache.  Results do not depend on what else runs. */
+
+/* One query per sequence, at position lens[b] - 1 (the decode step).
+ * q         device rows [batch], out device bf16 [batch][Hq][d]
+ * lens      device int32 [batch]; lengths above max_len are clamped to it,
+ *           a sequence of length 0 gets out = 0, lse = -inf
+ * Returns KVQ_ERR_UNSUPPORTED for batch or num_kv_heads above 65535. */
+int kvq_sink_decode_attention(const kvq_layout* layout, const kvq_cache* cache,
+                              const void* q, int q_dtype, int64_t q_stride, const int32_t* lens,
+                              int max_len, int sinks, int span, float sm_scale, void* out,
+                              float* lse, kvq_stream_t stream);
+
+/* A chunk of new queries per sequence, its newest positions, causal; the
+ * arguments that kvq_prefill_attention has mean the same here (the chunk's
+ * keys and values are appended and lens advanced first; query i of n_b sits
+ * at position lens[b] - n_b + i; sequences with n_b = 0, n_b > lens[b] or
+ * n_b > max_q are skipped and their rows left untouched).
+ * q         device rows [cu_q[batch]], out device bf16 [cu_q[batch]][Hq][d] */
+int kvq_sink_prefill_attention(const kvq_layout* layout, const kvq_cache* cache,
+                               const void* q, int q_dtype, int64_t q_stride, const int32_t* cu_q,
+                               const int32_t* lens, int max_q, int sinks, int span,
+                               float sm_scale, void* out, float* lse, kvq_stream_t stream);
+
+/* Read cached positions back as dense rows in the model's basis: rows
+ * cu_rows[b] .. cu_rows[b+1]-1 of k_out and v_out ([rows][Hkv][d], out_dtype
+ * KVQ_BF16 or KVQ_F32, rounded to nearest) get positions first[b],
+ * first[b] + 1, ... of sequence b: code*scale + zero (keys of rotated
+ * layouts rotated back, in fp32) or the bf16 rows of the ring.  The pages
+ * name dequantization into temporary storage ("Pertumbuhan cache ..."); in
+ * this form it moves a sequence to another layout or program.
+ * first     device int32 [batch], any value: positions below 0, at or past
+ *           lens[b], or on absent pages give rows of zeros
+ * cu_rows   device int32 [batch+1], non-decreasing, cu_rows[0] == 0
+ * max_rows  host bound on the rows of a sequence (launch size); a sequence
+ *           with more rows is skipped and its rows left untouched
+ * k_out, v_out 16-byte aligned.  Returns KVQ_ERR_UNSUPPORTED for batch
+ * above 65535 or num_kv_heads above 32767. */
+int kvq_read_back(const kvq_layout* layout, const kvq_cache* cache, const int32_t* first,
+                  const int32_t* cu_rows, const int32_t* lens, int max_rows, void* k_out,
+                  void* v_out, int out_dtype, kvq_stream_t stream);
+
 /* Rotate `rows` key rows [rows][Hkv... flattened][d] exactly as
  * kvq_quantize_append does before quantizing them (check path for the
  * key-only rotation of "Quantize What Counts", Resultaten).

@@ -74,6 +74,9 @@ def lib() -> C.CDLL:
         L.kvq_append_decode.argtypes = [LP, CP, P, P, I, P, P, I, P, I, P, I, C.c_float, P, P, P, S, P]
         L.kvq_dequantize.argtypes = [LP, CP, P, I, P, P, P]
         L.kvq_prefill_attention.argtypes = [LP, CP, P, I, P, P, I, C.c_float, P, P, P]
+        L.kvq_sink_decode_attention.argtypes = [LP, CP, P, I, C.c_int64, P, I, I, I, C.c_float, P, P, P]
+        L.kvq_sink_prefill_attention.argtypes = [LP, CP, P, I, C.c_int64, P, P, I, I, I, C.c_float, P, P, P]
+        L.kvq_read_back.argtypes = [LP, CP, P, P, P, I, P, P, I, P]
         L.kvq_rotate_keys.argtypes = [LP, P, I, I, P, P]
         L.kvq_set_decode_path.argtypes = [I]
         L.kvq_set_decode_path.restype = I
@@ -83,7 +86,7 @@ def lib() -> C.CDLL:
         L.kvq_decode_status.restype = I
         for n in ("kvq_page_bytes", "kvq_window_bytes", "kvq_quantize_append",
                   "kvq_decode_attention", "kvq_decode_attention_static_scratch", "kvq_append_decode",
-                  "kvq_dequantize",
+                  "kvq_dequantize", "kvq_sink_decode_attention", "kvq_sink_prefill_attention", "kvq_read_back",
                   "kvq_rotate_keys"):
             getattr(L, n).restype = I
         _lib_handle = L
@@ -136,6 +139,7 @@ def _check(t: Optional[torch.Tensor], name: str, dtypes, numel: Optional[int] = 
 _FLOAT_IN = (torch.bfloat16, torch.float32)
 _I32 = (torch.int32,)
 _F32 = (torch.float32,)
+_BF16 = (torch.bfloat16,)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -333,6 +337,73 @@ def kvq_prefill_attention(layout: Layout, cache: PagedCache, q: torch.Tensor, cu
           _ptr(cu_q), _ptr(lens), int(max_q), C.c_float(sm_scale), _ptr(out), _ptr(lse), _stream(stream))
 
 
+def _check_rows(q: torch.Tensor, name: str, rows: Optional[int], heads: int, d: int) -> Tuple[int, int]:
+    """q is [rows][heads][d] with dense [heads][d] rows that may lie apart
+    (a slice of a wider projection); returns (rows, elements between rows)."""
+    if not isinstance(q, torch.Tensor):
+        raise ValueError(f"{name} must be a torch.Tensor")
+    if q.dim() != 3 or q.shape[1] != heads or q.shape[2] != d or (rows is not None and q.shape[0] != rows):
+        raise ValueError(f"{name} must have shape [{'rows' if rows is None else rows}][{heads}][{d}], "
+                         f"got {list(q.shape)}")
+    if q.stride(2) != 1 or (heads > 1 and q.stride(1) != d):
+        raise ValueError(f"{name} must have contiguous [{heads}][{d}] rows, got strides {q.stride()}")
+    if q.device.type != "cuda" or q.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be a CUDA tensor on the current device, got {q.device}")
+    if q.dtype not in _FLOAT_IN:
+        raise ValueError(f"{name} must have dtype torch.bfloat16 or torch.float32, got {q.dtype}")
+    return q.shape[0], q.stride(0) if q.shape[0] > 1 else heads * d
+
+
+def kvq_sink_decode_attention(layout: Layout, cache: PagedCache, q: torch.Tensor, lens: torch.Tensor, max_len: int,
+                              sinks: int, span: int, sm_scale: float, out: torch.Tensor,
+                              lse: Optional[torch.Tensor], stream=None) -> None:
+    """kvq.h kvq_sink_decode_attention: q [B][Hq][d] (rows may lie apart) -> out bf16 [B][Hq][d], lse fp32 [B][Hq];
+    the query of a sequence sees its first `sinks` and its newest `span` cached positions."""
+    B, Hq, d = cache.batch, layout.num_q_heads, layout.head_dim
+    _, stride = _check_rows(q, "q", B, Hq, d)
+    _check(lens, "lens", _I32, B)
+    _check(out, "out", _BF16, B * Hq * d)
+    _check(lse, "lse", _F32, B * Hq, optional=True)
+    _call("kvq_sink_decode_attention", C.byref(layout.c()), C.byref(cache.c()), C.c_void_p(q.data_ptr()),
+          _dtype_code(q), stride, _ptr(lens), int(max_len), int(sinks), int(span), C.c_float(sm_scale), _ptr(out),
+          _ptr(lse), _stream(stream))
+
+
+def kvq_sink_prefill_attention(layout: Layout, cache: PagedCache, q: torch.Tensor, cu_q: torch.Tensor,
+                               lens: torch.Tensor, max_q: int, sinks: int, span: int, sm_scale: float,
+                               out: torch.Tensor, lse: Optional[torch.Tensor], stream=None) -> None:
+    """kvq.h kvq_sink_prefill_attention: each sequence's chunk of new queries (rows cu_q[b]..cu_q[b+1] of
+    q [total_q][Hq][d], rows may lie apart), causal, over its first `sinks` positions and the newest `span`
+    positions up to each query -> out bf16 [total_q][Hq][d], lse fp32 [total_q][Hq]."""
+    B, Hq, d = cache.batch, layout.num_q_heads, layout.head_dim
+    T, stride = _check_rows(q, "q", None, Hq, d)
+    _check(cu_q, "cu_q", _I32, B + 1)
+    _check(lens, "lens", _I32, B)
+    _check(out, "out", _BF16, T * Hq * d)
+    _check(lse, "lse", _F32, T * Hq, optional=True)
+    _call("kvq_sink_prefill_attention", C.byref(layout.c()), C.byref(cache.c()), C.c_void_p(q.data_ptr()),
+          _dtype_code(q), stride, _ptr(cu_q), _ptr(lens), int(max_q), int(sinks), int(span), C.c_float(sm_scale),
+          _ptr(out), _ptr(lse), _stream(stream))
+
+
+def kvq_read_back(layout: Layout, cache: PagedCache, first: torch.Tensor, cu_rows: torch.Tensor, lens: torch.Tensor,
+                  max_rows: int, k_out: torch.Tensor, v_out: torch.Tensor, stream=None) -> None:
+    """kvq.h kvq_read_back: positions first[b], first[b] + 1, ... of every sequence as rows
+    cu_rows[b]..cu_rows[b+1] of k_out and v_out [rows][Hkv][d] (bf16 or fp32), keys in the model's basis."""
+    B, row = cache.batch, layout.num_kv_heads * layout.head_dim
+    if k_out.dtype != v_out.dtype:
+        raise ValueError("k_out and v_out must share a dtype")
+    _check(k_out, "k_out", _FLOAT_IN)
+    if k_out.numel() % row:
+        raise ValueError(f"k_out must hold whole rows of {row} elements ([rows][Hkv][d])")
+    _check(v_out, "v_out", _FLOAT_IN, k_out.numel())
+    _check(first, "first", _I32, B)
+    _check(cu_rows, "cu_rows", _I32, B + 1)
+    _check(lens, "lens", _I32, B)
+    _call("kvq_read_back", C.byref(layout.c()), C.byref(cache.c()), _ptr(first), _ptr(cu_rows), _ptr(lens),
+          int(max_rows), _ptr(k_out), _ptr(v_out), _dtype_code(k_out), _stream(stream))
+
+
 def kvq_dequantize(layout: Layout, cache: PagedCache, lens: torch.Tensor, max_len: int,
                    k_out: torch.Tensor, v_out: torch.Tensor, stream=None) -> None:
     """kvq.h kvq_dequantize: fp32 [B][Hkv][max_len][d] reconstructions."""
@@ -417,6 +488,39 @@ def prefill_attention(layout: Layout, cache: PagedCache, q: torch.Tensor, cu_q: 
     return out, lse
 
 
+def sink_decode_attention(layout: Layout, cache: PagedCache, q: torch.Tensor, lens: torch.Tensor, max_len: int,
+                          sinks: int, span: int, sm_scale: Optional[float] = None, want_lse: bool = True):
+    """Allocating convenience wrapper around kvq_sink_decode_attention."""
+    out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if want_lse else None
+    kvq_sink_decode_attention(layout, cache, q, lens, max_len, sinks, span,
+                              layout.head_dim ** -0.5 if sm_scale is None else sm_scale, out, lse)
+    return out, lse
+
+
+def sink_prefill_attention(layout: Layout, cache: PagedCache, q: torch.Tensor, cu_q: torch.Tensor, lens: torch.Tensor,
+                           max_q: int, sinks: int, span: int, sm_scale: Optional[float] = None,
+                           want_lse: bool = True):
+    """Allocating convenience wrapper around kvq_sink_prefill_attention."""
+    out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if want_lse else None
+    kvq_sink_prefill_attention(layout, cache, q, cu_q, lens, max_q, sinks, span,
+                               layout.head_dim ** -0.5 if sm_scale is None else sm_scale, out, lse)
+    return out, lse
+
+
+def read_back(layout: Layout, cache: PagedCache, first: torch.Tensor, cu_rows: torch.Tensor, lens: torch.Tensor,
+              total_rows: int, max_rows: int, dtype: torch.dtype = torch.bfloat16):
+    """Allocating convenience wrapper around kvq_read_back: (keys, values) [total_rows][Hkv][d], where total_rows
+    is cu_rows[B] and max_rows bounds the rows of one sequence."""
+    shape = (int(total_rows), layout.num_kv_heads, layout.head_dim)
+    k = torch.empty(shape, dtype=dtype, device=lens.device)
+    v = torch.empty(shape, dtype=dtype, device=lens.device)
+    kvq_read_back(layout, cache, first, cu_rows, lens, max_rows, k, v)
+    return k, v
+
+
 __all__ = [n for n in dir() if n.startswith("kvq_")] + [
     "Layout", "PagedCache", "KVQError", "lib", "decode_attention", "prefill_attention", "workspace_for",
+    "sink_decode_attention", "sink_prefill_attention", "read_back",
     "LIB_PATH"]

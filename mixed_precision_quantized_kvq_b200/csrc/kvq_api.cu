@@ -9,6 +9,7 @@
 #include "kvq_internal.cuh"
 #include "kvq_channel.cuh"
 #include "kvq_prefill.cuh"
+#include "kvq_sink.cuh"
 
 namespace {
 
@@ -301,6 +302,68 @@ int kvq_prefill_attention(const kvq_layout* layout, const kvq_cache* cache, cons
     return cuda_status(kvq::launch_prefill_attention(p, layout->k_per_channel, 0, q, q_dtype == KVQ_BF16, cu_q, lens,
                                                      INT32_MAX, max_q, sm_scale, out, lse,
                                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// the checks that both forms of the attention with sinks share; *empty: nothing to do
+static int check_sink(const kvq_layout* layout, const kvq_cache* cache, const void* q, int q_dtype, int64_t q_stride,
+                      const int32_t* lens, int rows_bound, int sinks, int span, float sm_scale, const void* out,
+                      const float* lse, bool* empty) {
+    int rc = check_layout(layout);
+    if (rc) return rc;
+    if ((rc = check_cache(layout, cache))) return rc;
+    if (q_dtype != KVQ_F32 && q_dtype != KVQ_BF16) return KVQ_ERR_INVALID_ARG;
+    if (!lens || rows_bound < 0 || sinks < 0 || span < 0 || !isfinite(sm_scale)) return KVQ_ERR_INVALID_ARG;
+    if (cache->batch > 65535 || layout->num_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+    *empty = cache->batch == 0 || rows_bound == 0;
+    if (*empty) return KVQ_OK;
+    if (!q || !out || !aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+        return KVQ_ERR_INVALID_ARG;
+    const int64_t row = int64_t(layout->num_q_heads) * layout->head_dim;
+    if (q_stride < row || q_stride > (int64_t(1) << 40) || q_stride % (q_dtype == KVQ_BF16 ? 8 : 4))
+        return KVQ_ERR_INVALID_ARG;
+    return KVQ_OK;
+}
+
+int kvq_sink_decode_attention(const kvq_layout* layout, const kvq_cache* cache, const void* q, int q_dtype,
+                              int64_t q_stride, const int32_t* lens, int max_len, int sinks, int span, float sm_scale,
+                              void* out, float* lse, kvq_stream_t stream) {
+    bool empty = false;
+    if (max_len < 0) return KVQ_ERR_INVALID_ARG;
+    const int rc = check_sink(layout, cache, q, q_dtype, q_stride, lens, 1, sinks, span, sm_scale, out, lse, &empty);
+    if (rc || empty) return rc;
+    const Params p = make_params(layout, cache);
+    kvq::sink::Args a{q, q_dtype == KVQ_BF16, q_stride, nullptr, lens, max_len, 1, sinks, span,
+                      sm_scale * 1.4426950408889634f, static_cast<__nv_bfloat16*>(out), lse, layout->k_per_channel};
+    return cuda_status(kvq::launch_sink_attention(p, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kvq_sink_prefill_attention(const kvq_layout* layout, const kvq_cache* cache, const void* q, int q_dtype,
+                               int64_t q_stride, const int32_t* cu_q, const int32_t* lens, int max_q, int sinks,
+                               int span, float sm_scale, void* out, float* lse, kvq_stream_t stream) {
+    bool empty = false;
+    if (!cu_q) return KVQ_ERR_INVALID_ARG;
+    const int rc = check_sink(layout, cache, q, q_dtype, q_stride, lens, max_q, sinks, span, sm_scale, out, lse, &empty);
+    if (rc || empty) return rc;
+    const Params p = make_params(layout, cache);
+    kvq::sink::Args a{q, q_dtype == KVQ_BF16, q_stride, cu_q, lens, INT32_MAX, max_q, sinks, span,
+                      sm_scale * 1.4426950408889634f, static_cast<__nv_bfloat16*>(out), lse, layout->k_per_channel};
+    return cuda_status(kvq::launch_sink_attention(p, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kvq_read_back(const kvq_layout* layout, const kvq_cache* cache, const int32_t* first, const int32_t* cu_rows,
+                  const int32_t* lens, int max_rows, void* k_out, void* v_out, int out_dtype, kvq_stream_t stream) {
+    int rc = check_layout(layout);
+    if (rc) return rc;
+    if ((rc = check_cache(layout, cache))) return rc;
+    if (out_dtype != KVQ_F32 && out_dtype != KVQ_BF16) return KVQ_ERR_INVALID_ARG;
+    if (!first || !cu_rows || !lens || max_rows < 0 || max_rows > INT32_MAX - 128) return KVQ_ERR_INVALID_ARG;
+    if (cache->batch > 65535 || layout->num_kv_heads > 32767) return KVQ_ERR_UNSUPPORTED;
+    if (cache->batch == 0 || max_rows == 0) return KVQ_OK;
+    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return KVQ_ERR_INVALID_ARG;
+    const Params p = make_params(layout, cache);
+    const kvq::ReadBackArgs a{first, cu_rows, lens, max_rows, k_out, v_out, out_dtype == KVQ_BF16,
+                              layout->k_per_channel};
+    return cuda_status(kvq::launch_read_back(p, a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int kvq_dequantize(const kvq_layout* layout, const kvq_cache* cache, const int32_t* lens, int max_len,
