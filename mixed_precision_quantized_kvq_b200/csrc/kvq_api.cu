@@ -334,7 +334,7 @@ int kvq_sink_decode_attention(const kvq_layout* layout, const kvq_cache* cache, 
     const Params p = make_params(layout, cache);
     kvq::sink::Args a{q, q_dtype == KVQ_BF16, q_stride, nullptr, lens, max_len, 1, sinks, span,
                       sm_scale * 1.4426950408889634f, static_cast<__nv_bfloat16*>(out), lse, layout->k_per_channel};
-    return cuda_status(kvq::launch_sink_attention(p, a, reinterpret_cast<cudaStream_t>(stream)));
+    return cuda_status(kvq::launch_sink_attention(p, a, device_sm_count(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int kvq_sink_prefill_attention(const kvq_layout* layout, const kvq_cache* cache, const void* q, int q_dtype,
@@ -347,7 +347,7 @@ int kvq_sink_prefill_attention(const kvq_layout* layout, const kvq_cache* cache,
     const Params p = make_params(layout, cache);
     kvq::sink::Args a{q, q_dtype == KVQ_BF16, q_stride, cu_q, lens, INT32_MAX, max_q, sinks, span,
                       sm_scale * 1.4426950408889634f, static_cast<__nv_bfloat16*>(out), lse, layout->k_per_channel};
-    return cuda_status(kvq::launch_sink_attention(p, a, reinterpret_cast<cudaStream_t>(stream)));
+    return cuda_status(kvq::launch_sink_attention(p, a, device_sm_count(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int kvq_read_back(const kvq_layout* layout, const kvq_cache* cache, const int32_t* first, const int32_t* cu_rows,

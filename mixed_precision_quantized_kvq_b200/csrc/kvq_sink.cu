@@ -77,7 +77,21 @@ __global__ void sink_attention_kernel(Params p, sink::Args a) {
 
 }  // namespace
 
-cudaError_t launch_sink_attention(const Params& p, const sink::Args& a, cudaStream_t s) {
+cudaError_t launch_sink_decode_k1(const Params&, const sink::Args&, int, cudaStream_t);
+cudaError_t launch_sink_decode_k2(const Params&, const sink::Args&, int, cudaStream_t);
+cudaError_t launch_sink_decode_k4(const Params&, const sink::Args&, int, cudaStream_t);
+cudaError_t launch_sink_decode_k8(const Params&, const sink::Args&, int, cudaStream_t);
+
+cudaError_t launch_sink_attention(const Params& p, const sink::Args& a, int sms, cudaStream_t s) {
+    // one query per sequence, scales shared by 32 channels or more
+    if (!a.cu_q && !a.kpc && p.kg >= 32) {
+        switch (p.kb) {
+            case 1: return launch_sink_decode_k1(p, a, sms, s);
+            case 2: return launch_sink_decode_k2(p, a, sms, s);
+            case 4: return launch_sink_decode_k4(p, a, sms, s);
+            default: return launch_sink_decode_k8(p, a, sms, s);
+        }
+    }
     const dim3 grid(a.max_q, p.hkv, p.batch);
     if (p.d == 128)
         sink_attention_kernel<128><<<grid, 32 * p.g, 0, s>>>(p, a);

@@ -60,7 +60,7 @@ __device__ __forceinline__ bool sequence(const Args& a, int b, Seq& s) {
 
 }  // namespace sink
 
-cudaError_t launch_sink_attention(const Params& p, const sink::Args& a, cudaStream_t s);
+cudaError_t launch_sink_attention(const Params& p, const sink::Args& a, int sms, cudaStream_t s);
 
 // kvq_read_back: rows [cu_rows[b], cu_rows[b+1]) get positions first[b] ...
 struct ReadBackArgs {
