@@ -20,8 +20,8 @@
 //
 // Work split: one cluster of 1 to 8 CTAs per (sequence, kv-head); its warps
 // take the 64-position pages in turn (warp w of W: pages w, w + W, ...), then
-// 16-slot pieces of the bf16 ring, each warp with its own ring of kStages
-// shared-memory stages filled by cp.async.  The warps' partial sums meet in
+// 16-slot pieces of the bf16 ring, each with its own buffers for keys and
+// values filled by cp.async.  The warps' partial sums meet in
 // shared memory, across the cluster through distributed shared memory: no
 // workspace, no atomics, the same result on every run.
 //
@@ -47,8 +47,7 @@ namespace sink {
 
 using namespace ptx;
 
-constexpr int kStages = 2;
-constexpr int kMaxWarps = 12;          // of a CTA, and what the registers of an SM hold
+constexpr int kMaxWarps = 16;          // what the registers of an SM hold, in one CTA or several
 constexpr int kHeads = 8;            // columns of the products
 constexpr int kRing = 16;            // ring slots per piece
 constexpr float kRefNone = -1e30f;   // reference exponent before any position
@@ -57,44 +56,43 @@ constexpr unsigned kAll = 0xffffffffu;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_f16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(b0));
 }
+// the same without volatile, so that the compiler may move loads and masks across it
+__device__ __forceinline__ void mma_b16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
+}
+__device__ __forceinline__ void cp8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
+// the kernels' view of shared memory: byte pointers
+__device__ __forceinline__ uint32_t lds32(const unsigned char* a) { return *reinterpret_cast<const uint32_t*>(a); }
+__device__ __forceinline__ uint2 lds64(const unsigned char* a) { return *reinterpret_cast<const uint2*>(a); }
+__device__ __forceinline__ uint4 lds128(const unsigned char* a) { return *reinterpret_cast<const uint4*>(a); }
+__device__ __forceinline__ void sts32(unsigned char* a, uint32_t v) { *reinterpret_cast<uint32_t*>(a) = v; }
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
     __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&h);
@@ -109,11 +107,39 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ float low_half(uint32_t w) { return __low2float(*reinterpret_cast<__half2*>(&w)); }
 
-// position (of eight) in row x of a score tile
+// Position of row x of the T-th eight rows of a page's scores.  Rows 2c and 2c + 1 are the positions of code pair T of
+// the value words that lane column c holds (word c of a run's 16 bytes; half of word c >> 1 for 1-bit values): the
+// weights of a pair then sit in one register after the transposition, and one mask takes the two codes out.
 template <int VB>
-__device__ __forceinline__ constexpr int row_position(int x) {
-    return VB == 4 ? (x >> 1) + 4 * (x & 1) : VB == 8 ? 4 * (x >> 2) + ((x >> 1) & 1) + 2 * (x & 1) : x;
+__device__ __forceinline__ int row_position(int T, int x) {
+    if (VB == 8) return 16 * (T >> 1) + 2 * x + (T & 1);
+    if (VB == 4) return 32 * (T >> 2) + 4 * x + (T & 3);
+    if (VB == 2) return 8 * x + T;
+    return 32 * (x >> 2) + 8 * ((x >> 1) & 1) + 16 * (x & 1) + T;
 }
+// The bit at which pair T sits in its word (1-bit and the upper 2-bit pairs: after a shift) is value_bit.
+// A lane column's 16 positions as four runs of four (the first position of run i), and where the words of pair T are
+// among the 16 (the second kPairWords further).
+template <int VB>
+__device__ __forceinline__ int value_run(int c, int i) {
+    if (VB == 8) return 16 * i + 4 * c;
+    if (VB == 4) return 32 * (i >> 1) + 8 * c + 4 * (i & 1);
+    if (VB == 2) return 16 * c + 4 * i;
+    return 32 * (c >> 1) + 8 * (c & 1) + 16 * (i >> 1) + 4 * (i & 1);
+}
+template <int VB>
+__device__ __forceinline__ constexpr int pair_word(int T) {
+    return VB == 8 ? 4 * (T >> 1) + (T & 1) : VB == 4 ? 8 * (T >> 2) + (T & 3) : T;
+}
+template <int VB>
+constexpr int kPairWords = VB == 8 ? 2 : VB == 4 ? 4 : 8;
+template <int VB>
+__device__ __forceinline__ constexpr int value_bit(int T) {
+    return VB == 8 ? 0 : VB == 4 ? 4 * (T & 1) : VB == 2 ? (T < 5 ? 2 * T : 2 * T - 10) : T;
+}
+// Key rows and their metadata are stored with their 16-byte pieces exchanged within each 128 bytes, so that the eight
+// positions of a score tile, whichever they are, lie in different banks.
+__device__ __forceinline__ int key_slot(int t) { return t ^ ((t >> 3) & 7); }
 
 // channels of code pair i (0..3) of lane column c within 32 channels, and the bit position of the pair
 template <int KB>
@@ -128,8 +154,8 @@ __device__ __forceinline__ constexpr int pair_bit(int i) {
     return KB == 4 ? 4 * (i & 1) : KB == 2 ? 2 * i : KB == 1 ? i : 0;
 }
 
-// Shared memory of a CTA of W warps: query fragments' sources, then the
-// warps' stages; the partial sums take the stages' place at the end.
+// Shared memory of a CTA: what the query fragments are made of, then the
+// warps' buffers; the partial sums take the buffers' place at the end.
 template <int D>
 struct Head {
     __half qh[kHeads][D];                    // query, scaled to at most 2^8 per head, high and low part
@@ -140,24 +166,30 @@ struct Head {
     float factor[kHeads];                    // score scale * log2(e) / query scaling
 };
 
+// A warp's buffers: keys (codes and metadata, or 16 ring rows) and values.  While the values are worked on, the next
+// keys come in, and the other way round.
 template <int D, int KB, int VB>
-struct Stage {
-    static constexpr int kK = kPage * D * KB / 8, kV = kPage * D * VB / 8;
-    static constexpr int kRingBytes = 2 * kRing * 2 * D;
-    __host__ __device__ static int bytes(const Params& p) {
-        const int page = kK + kV + kPage * 4 * (p.nkg + p.nvg);
-        return page > kRingBytes ? page : kRingBytes;
-    }
+struct Buf {
+    static constexpr int kK = kPage * D * KB / 8, kV = kPage * D * VB / 8, kRows = kRing * 2 * D;
+    static constexpr int kUnits = D / 32;      // key metadata is kept for every 32 channels, value metadata by groups
+    static constexpr int keys() { return max_of(kK + kPage * 4 * kUnits, kRows); }
+    __host__ __device__ static int values(const Params& p) { return max_of(kV + kPage * 4 * p.nvg, kRows); }
+    __host__ __device__ static constexpr int max_of(int a, int b) { return a > b ? a : b; }
 };
 
 // partial sums of a warp: [head][D] values, then reference exponents and sums of the weights
 template <int D>
 constexpr int kPartFloats = kHeads * D + 2 * kHeads;
 
+// bytes of a warp's part of shared memory, and of a CTA's
+template <int D, int KB, int VB>
+__host__ __device__ int warp_smem(const Params& p) {
+    const int both = Buf<D, KB, VB>::keys() + Buf<D, KB, VB>::values(p), part = kPartFloats<D> * 4;
+    return both > part ? both : part;
+}
 template <int D, int KB, int VB>
 __host__ __device__ int decode_smem(const Params& p, int warps) {
-    const int stage = Stage<D, KB, VB>::bytes(p) * kStages, part = kPartFloats<D> * 4;
-    return int(sizeof(Head<D>)) + warps * (stage > part ? stage : part);
+    return int(sizeof(Head<D>)) + warps * warp_smem<D, KB, VB>(p);
 }
 
 // The running state of a warp: fragments of the output (channels 16*i + r, 16*i + r + 8 of heads 2c, 2c+1; scaled by
@@ -208,82 +240,72 @@ __device__ __forceinline__ float sum_rows(float x) {
 // visible to the query: position x below `limit` of the part it lives in
 __device__ __forceinline__ bool visible(int x, int ns, int lo, int limit) { return x < limit && (x < ns || x >= lo); }
 
-// one 64-position page in the stage at `st`: base = position of slot 0
+// Scores of one 64-position page whose keys are at `sk` (base = position of slot 0), to be multiplied by the head's
+// factor: s[T][e] is position row_position(T, r), head 2c + e.
 template <int D, int KB, int VB, bool LO>
-__device__ __forceinline__ void page_tile(const Params& p, uint32_t st, int base, int ns, int lo, int Lq, bool edge,
-                                          const uint32_t (&qh)[D / 8], const uint32_t (&ql)[LO ? D / 8 : 1],
-                                          uint32_t qz, const float (&factor)[2], Sums<D>& S) {
-    using G = Stage<D, KB, VB>;
+__device__ __forceinline__ void page_scores(const Params& p, unsigned char* sk, int base, int ns, int lo, int Lq, bool edge,
+                                            const uint32_t (&qh)[D / 8], const uint32_t (&ql)[LO ? D / 8 : 1], uint32_t qz,
+                                            float (&s)[8][2]) {
     constexpr int NU = D / 32;
     const int lane = threadIdx.x % 32, r = lane >> 2, c = lane & 3;
-    const int nkg = p.nkg, nvg = p.nvg;
-    const uint32_t sk = st, sv = st + G::kK, skm = sv + G::kV, svm = skm + kPage * 4 * nkg;
-    if (edge) {   // positions that are not visible: finite scores (masked below) and no values
+    unsigned char* skm = sk + Buf<D, KB, VB>::kK;
+    const auto meta = [&](int t) { return skm + key_slot(t) * (NU * 4); };
+    if (edge) {   // positions that are not visible: finite scores (masked below)
         for (int t = lane; t < kPage; t += 32)
-            if (!visible(base + t, ns, lo, Lq)) {
-                for (int i = 0; i < nkg; ++i) sts32(skm + (t * nkg + i) * 4, 0);
-                for (int i = 0; i < nvg; ++i) sts32(svm + (t * nvg + i) * 4, 0);
-            }
+            if (!visible(base + t, ns, lo, Lq))
+                for (int i = 0; i < NU; ++i) sts32(meta(t) + i * 4, 0);
         __syncwarp();
     }
-    const int perm = row_position<VB>(r);
-    // ---- scores: four tiles of 16 positions ----
-    float s[4][4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const int t0 = 16 * b + perm, t1 = t0 + 8;      // positions of rows r and r + 8
+    for (int b = 0; b < 4; ++b) {                       // 16 positions: rows r and r + 8
+        const int t0 = row_position<VB>(2 * b, r), t1 = row_position<VB>(2 * b + 1, r);
         uint32_t m0[4], m1[4];                          // metadata of the 32-channel units
-        if (nkg == 4) {
-            const uint4 x = lds128(skm + t0 * 16), y = lds128(skm + t1 * 16);
+        if (NU == 4) {
+            const uint4 x = lds128(meta(t0)), y = lds128(meta(t1));
             m0[0] = x.x, m0[1] = x.y, m0[2] = x.z, m0[3] = x.w;
             m1[0] = y.x, m1[1] = y.y, m1[2] = y.z, m1[3] = y.w;
         } else {
-            const int sh = nkg == NU ? 0 : nkg * 2 == NU ? 1 : 2;
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                m0[u] = lds32(skm + (t0 * nkg + (u >> sh)) * 4);
-                m1[u] = lds32(skm + (t1 * nkg + (u >> sh)) * 4);
-            }
+            const uint2 x = lds64(meta(t0)), y = lds64(meta(t1));
+            m0[0] = x.x, m0[1] = x.y, m1[0] = y.x, m1[1] = y.y;
         }
         // zero points of units 2(c & 1), 2(c & 1) + 1 against the unit sums (high parts at c < 2, low at c >= 2)
         float z[4] = {0.f, 0.f, 0.f, 0.f};
-        if (NU == 4) {
-            const bool odd = c & 1;
+        const bool odd = c & 1;
+        if (NU == 4)
             mma_f16_k8(z, __byte_perm(odd ? m0[2] : m0[0], odd ? m0[NU - 1] : m0[1], 0x7632),
                        __byte_perm(odd ? m1[2] : m1[0], odd ? m1[NU - 1] : m1[1], 0x7632), qz);
-        } else {
-            mma_f16_k8(z, (c & 1) ? 0u : __byte_perm(m0[0], m0[1], 0x7632), (c & 1) ? 0u : __byte_perm(m1[0], m1[1], 0x7632),
-                       qz);
-        }
+        else
+            mma_f16_k8(z, odd ? 0u : __byte_perm(m0[0], m0[1], 0x7632), odd ? 0u : __byte_perm(m1[0], m1[1], 0x7632), qz);
         float a[4] = {0.f, 0.f, 0.f, 0.f};
+        const unsigned char *k0 = sk + key_slot(t0) * (KB == 1 ? D / 8 : 16), *k1 = sk + key_slot(t1) * (KB == 1 ? D / 8 : 16);
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
             uint32_t e[4], f[4];                        // code pairs of rows r and r + 8
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int t = h ? t1 : t0;
+                const unsigned char* k = h ? k1 : k0;
                 uint32_t(&x)[4] = h ? f : e;
                 if (KB == 8) {
-                    const uint32_t w0 = lds32(sk + (2 * u) * (kPage * 16) + t * 16 + c * 4);
-                    const uint32_t w1 = lds32(sk + (2 * u + 1) * (kPage * 16) + t * 16 + c * 4);
+                    const uint32_t w0 = lds32(k + (2 * u) * (kPage * 16) + c * 4);
+                    const uint32_t w1 = lds32(k + (2 * u + 1) * (kPage * 16) + c * 4);
                     x[0] = w0 & 0x00ff00ffu;
                     x[1] = (w0 >> 8) & 0x00ff00ffu;
                     x[2] = w1 & 0x00ff00ffu;
                     x[3] = (w1 >> 8) & 0x00ff00ffu;
                 } else if (KB == 4) {
-                    const uint32_t w = lds32(sk + u * (kPage * 16) + t * 16 + c * 4), v = w >> 8;
+                    const uint32_t w = lds32(k + u * (kPage * 16) + c * 4), v = w >> 8;
                     x[0] = w & 0x000f000fu;
                     x[1] = w & 0x00f000f0u;
                     x[2] = v & 0x000f000fu;
                     x[3] = v & 0x00f000f0u;
                 } else if (KB == 2) {
-                    const uint32_t w = lds32(sk + (u >> 1) * (kPage * 16) + t * 16 + (2 * (u & 1) + (c >> 1)) * 4) >> (8 * (c & 1));
+                    const uint32_t w = lds32(k + (u >> 1) * (kPage * 16) + (2 * (u & 1) + (c >> 1)) * 4) >> (8 * (c & 1));
                     x[0] = w & 0x00030003u;
                     x[1] = w & 0x000c000cu;
                     x[2] = w & 0x00300030u;
                     x[3] = w & 0x00c000c0u;
                 } else {
-                    const uint32_t w = lds32(sk + t * (D / 8) + u * 4) >> (4 * c);
+                    const uint32_t w = lds32(k + u * 4) >> (4 * c);
                     x[0] = w & 0x00010001u;
                     x[1] = w & 0x00020002u;
                     x[2] = w & 0x00040004u;
@@ -304,69 +326,68 @@ __device__ __forceinline__ void page_tile(const Params& p, uint32_t st, int base
             a[3] = fmaf(s1, d[3], a[3]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[b][i] = fmaf(a[i], kCode, z[i]) * factor[i & 1];
+        for (int i = 0; i < 4; ++i) s[2 * b + (i >> 1)][i & 1] = fmaf(a[i], kCode, z[i]);
         if (edge) {
-            if (!visible(base + t0, ns, lo, Lq)) s[b][0] = s[b][1] = -INFINITY;
-            if (!visible(base + t1, ns, lo, Lq)) s[b][2] = s[b][3] = -INFINITY;
+            if (!visible(base + t0, ns, lo, Lq)) s[2 * b][0] = s[2 * b][1] = -INFINITY;
+            if (!visible(base + t1, ns, lo, Lq)) s[2 * b + 1][0] = s[2 * b + 1][1] = -INFINITY;
         }
     }
-    // ---- weights ----
+}
+
+// The weights of the scores and the product with the values at `sv`.
+template <int D, int KB, int VB>
+__device__ __forceinline__ void page_values(const Params& p, unsigned char* sv, int base, int ns, int lo, int Lq, bool edge,
+                                            const float (&s)[8][2], const float (&factor)[2], Sums<D>& S) {
+    const int lane = threadIdx.x % 32, r = lane >> 2, c = lane & 3, nvg = p.nvg;
+    unsigned char* svm = sv + Buf<D, KB, VB>::kV;
+    const int vshift = __ffs(p.vg) - 1;
+    if (edge) {   // no values at positions that are not visible
+        for (int t = lane; t < kPage; t += 32)
+            if (!visible(base + t, ns, lo, Lq))
+                for (int i = 0; i < nvg; ++i) sts32(svm + (i * kPage + t) * 4, 0);
+        __syncwarp();
+    }
     float top[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        float x = fmaxf(s[0][e], s[0][e + 2]);
+        float x = s[0][e];
 #pragma unroll
-        for (int b = 1; b < 4; ++b) x = fmaxf(x, fmaxf(s[b][e], s[b][e + 2]));
-        top[e] = max_rows(x);
+        for (int T = 1; T < 8; ++T) x = fmaxf(x, s[T][e]);
+        top[e] = max_rows(x) * factor[e];                // factors are not negative
     }
     uint32_t vmax = 0;                                   // largest value scale, as its fp16 bits
     for (int i = lane; i < kPage * nvg; i += 32) vmax = max(vmax, lds32(svm + i * 4) & 0x7fffu);
     vmax = __reduce_max_sync(kAll, vmax);
     raise_ref(S, top, max(0, int(vmax >> 10) - 14));     // a scale is below 2^(exponent field - 14)
-    uint32_t w[8];                                       // weights (positions of rows 2c, 2c+1; head r) of eight positions
+    uint32_t w[8];                                       // weights of pair T, head r
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float p0 = ex2(s[b][2 * h] - S.ref[0]), p1 = ex2(s[b][2 * h + 1] - S.ref[1]);
-            S.l[0] += p0;
-            S.l[1] += p1;
-            w[2 * b + h] = transpose8(half2_bits(p0, p1));
-        }
-    // B registers: the two positions whose codes one mask takes out of a value word
-    uint32_t B[8];
-    int tok[8];                                          // position of the low half; the high half is `gap` further
-    constexpr int gap = VB == 8 ? 2 : VB == 4 ? 4 : VB == 2 ? 8 : 16;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (VB >= 4) {
-            B[j] = w[j];
-            tok[j] = 8 * j + (VB == 4 ? c : 4 * (c >> 1) + (c & 1));
-        } else if (VB == 2) {
-            B[j] = __byte_perm(w[j & ~1], w[j | 1], (j & 1) ? 0x7632 : 0x5410);
-            tok[j] = 16 * (j >> 1) + 2 * c + (j & 1);
-        } else {
-            const int wd = j >> 2, hh = (j >> 1) & 1;
-            B[j] = __byte_perm(w[4 * wd + hh], w[4 * wd + hh + 2], (j & 1) ? 0x7632 : 0x5410);
-            tok[j] = 32 * wd + 8 * hh + 2 * c + (j & 1);
-        }
+    for (int T = 0; T < 8; ++T) {
+        const float p0 = ex2(fmaf(s[T][0], factor[0], -S.ref[0])), p1 = ex2(fmaf(s[T][1], factor[1], -S.ref[1]));
+        S.l[0] += p0;
+        S.l[1] += p1;
+        w[T] = transpose8(half2_bits(p0, p1));
     }
-    // ---- values ----
     uint32_t Z[8], pv[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) Z[j] = 0;
+    for (int T = 0; T < 8; ++T) Z[T] = 0;
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt) {
-        if (16 * mt % p.vg == 0) {
-            const int gi = 16 * mt / p.vg;
+        if ((16 * mt & (p.vg - 1)) == 0) {
+            const int gi = 16 * mt >> vshift;
+            // metadata of this lane's 16 positions, four neighbours a load
+            uint32_t m[16];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t x = lds32(svm + (tok[j] * nvg + gi) * 4), y = lds32(svm + ((tok[j] + gap) * nvg + gi) * 4);
-                pv[j] = hmul2(B[j], __byte_perm(x, y, 0x5410));
-                // odd pairs of 2-bit and 1-bit codes sit at bit 2 and bit 1
-                if (VB == 2 && (j & 1)) pv[j] = hmul2(pv[j], 0x34003400u);
-                if (VB == 1 && (j & 1)) pv[j] = hmul2(pv[j], 0x38003800u);
-                if (r == gi) Z[j] = __byte_perm(x, y, 0x7632);
+            for (int i = 0; i < 4; ++i) {
+                const uint4 x = lds128(svm + gi * (kPage * 4) + value_run<VB>(c, i) * 4);
+                m[4 * i] = x.x, m[4 * i + 1] = x.y, m[4 * i + 2] = x.z, m[4 * i + 3] = x.w;
+            }
+#pragma unroll
+            for (int T = 0; T < 8; ++T) {
+                const uint32_t x = m[pair_word<VB>(T)], y = m[pair_word<VB>(T) + kPairWords<VB>];
+                pv[T] = hmul2(w[T], __byte_perm(x, y, 0x5410));
+                if (value_bit<VB>(T))                    // the power of two of the codes' position
+                    pv[T] = hmul2(pv[T], uint32_t(15 - value_bit<VB>(T)) * 0x04000400u);
+                if (r == gi) Z[T] = __byte_perm(x, y, 0x7632);
             }
         }
         uint32_t e[8], f[8];                             // code pairs of channels 16*mt + r and + 8
@@ -376,38 +397,35 @@ __device__ __forceinline__ void page_tile(const Params& p, uint32_t st, int base
             uint32_t(&x)[8] = h ? f : e;
             if (VB == 8) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[j] = (lds32(sv + (j >> 1) * (D * 16) + ch * 16 + (2 * (j & 1) + (c >> 1)) * 4) >> (8 * (c & 1))) & 0x00ff00ffu;
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t v = lds32(sv + j * (D * 16) + ch * 16 + c * 4);
+                    x[2 * j] = v & 0x00ff00ffu;
+                    x[2 * j + 1] = (v >> 8) & 0x00ff00ffu;
+                }
             } else if (VB == 4) {
-                const uint4 u = lds128(sv + ch * 16), v = lds128(sv + D * 16 + ch * 16);
-                const uint32_t wd[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = (wd[j] >> (4 * c)) & 0x000f000fu;
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t v = lds32(sv + j * (D * 16) + ch * 16 + c * 4), u = v >> 8;
+                    x[4 * j] = v & 0x000f000fu;
+                    x[4 * j + 1] = v & 0x00f000f0u;
+                    x[4 * j + 2] = u & 0x000f000fu;
+                    x[4 * j + 3] = u & 0x00f000f0u;
+                }
             } else if (VB == 2) {
-                const uint4 u = lds128(sv + ch * 16);
-                const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
+                const uint32_t v = lds32(sv + ch * 16 + c * 4), u = v >> 10;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t v = wd[j] >> (4 * c);
-                    x[2 * j] = v & 0x00030003u;
-                    x[2 * j + 1] = v & 0x000c000cu;
-                }
+                for (int T = 0; T < 8; ++T) x[T] = (T < 5 ? v : u) & (0x00030003u << value_bit<VB>(T));
             } else {
-                const uint2 u = lds64(sv + ch * 8);
-                const uint32_t wd[2] = {u.x, u.y};
+                const uint32_t v = lds32(sv + ch * 8 + (c >> 1) * 4) >> (8 * (c & 1));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t v = wd[j >> 1] >> (2 * c + 8 * (j & 1));
-                    x[2 * j] = v & 0x00010001u;
-                    x[2 * j + 1] = v & 0x00020002u;
-                }
+                for (int T = 0; T < 8; ++T) x[T] = v & (0x00010001u << T);
             }
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) mma_f16(S.acc[mt], e[2 * k], f[2 * k], e[2 * k + 1], f[2 * k + 1], pv[2 * k], pv[2 * k + 1]);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) mma_f16(S.zero, Z[2 * k], 0, Z[2 * k + 1], 0, B[2 * k], B[2 * k + 1]);
+    for (int k = 0; k < 4; ++k) mma_f16(S.zero, Z[2 * k], 0, Z[2 * k + 1], 0, w[2 * k], w[2 * k + 1]);
 }
 
 // Where 16-byte piece o of ring row i lies: exchanged within the row so that the same piece of eight rows falls into
@@ -417,40 +435,43 @@ __device__ __forceinline__ int ring_piece(int i, int o) {
     return i * (2 * D) + ((o ^ (((i & 1) << 2) | ((i >> 1) & 3))) << 4);
 }
 
-// 16 ring slots in the stage at `st`; ok: bit i set when slot i holds a visible position (other rows are zeros)
+// Scores of 16 ring slots whose keys are at `sk`: s[h][e] is slot 8h + r, head 2c + e.  ok: bit i set when slot i holds
+// a visible position (other rows are zeros).
 template <int D>
-__device__ __forceinline__ void ring_tile(const Head<D>& hd, uint32_t st, uint32_t ok, bool lo_part, float scale_log2,
-                                          Sums<D>& S) {
+__device__ __forceinline__ void ring_scores(const Head<D>& hd, const unsigned char* sk, uint32_t ok, bool lo_part,
+                                            float scale_log2, float (&out)[8][2]) {
     const int lane = threadIdx.x % 32, r = lane >> 2, c = lane & 3;
-    const uint32_t sv = st + kRing * 2 * D;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {                   // channels 32*j + 8*c .. + 7 in one 16-byte piece
-        const uint4 k0 = lds128(st + ring_piece<D>(r, 4 * j + c)), k1 = lds128(st + ring_piece<D>(r + 8, 4 * j + c));
+        const uint4 k0 = lds128(sk + ring_piece<D>(r, 4 * j + c)), k1 = lds128(sk + ring_piece<D>(r + 8, 4 * j + c));
         const uint4 q = *reinterpret_cast<const uint4*>(&hd.bh[r][32 * j + 8 * c]);
         uint32_t a[4] = {k0.x, k1.x, k0.y, k1.y}, b[4] = {k0.z, k1.z, k0.w, k1.w};
-        mma_bf16(s, a, q.x, q.y);
-        mma_bf16(s, b, q.z, q.w);
+        mma_b16(s, a, q.x, q.y);
+        mma_b16(s, b, q.z, q.w);
         if (lo_part) {
             const uint4 ql = *reinterpret_cast<const uint4*>(&hd.bl[r][32 * j + 8 * c]);
-            mma_bf16(s, a, ql.x, ql.y);
-            mma_bf16(s, b, ql.z, ql.w);
+            mma_b16(s, a, ql.x, ql.y);
+            mma_b16(s, b, ql.z, ql.w);
         }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = (ok >> (r + 8 * (i >> 1))) & 1u ? s[i] * scale_log2 : -INFINITY;
-    const float top[2] = {max_rows(fmaxf(s[0], s[2])), max_rows(fmaxf(s[1], s[3]))};
+    for (int i = 0; i < 4; ++i) out[i >> 1][i & 1] = (ok >> (r + 8 * (i >> 1))) & 1u ? s[i] * scale_log2 : -INFINITY;
+}
+
+template <int D>
+__device__ __forceinline__ void ring_values(const unsigned char* sv, const float (&s)[8][2], Sums<D>& S) {
+    const int lane = threadIdx.x % 32;
+    const float top[2] = {max_rows(fmaxf(s[0][0], s[1][0])), max_rows(fmaxf(s[0][1], s[1][1]))};
     raise_ref(S, top, 0);
-    float p[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = ex2(s[i] - S.ref[i & 1]);
-    S.l[0] += p[0] + p[2];
-    S.l[1] += p[1] + p[3];
     // weights as bf16 high and low parts, in the output's unit of 2^-24
     uint32_t wh[2], wl[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const float x = p[2 * h] * (1.f / kCode), y = p[2 * h + 1] * (1.f / kCode);
+        const float p0 = ex2(s[h][0] - S.ref[0]), p1 = ex2(s[h][1] - S.ref[1]);
+        S.l[0] += p0;
+        S.l[1] += p1;
+        const float x = p0 * (1.f / kCode), y = p1 * (1.f / kCode);
         const uint32_t hi = bf162_bits(x, y);
         wh[h] = transpose8(hi);
         wl[h] = transpose8(bf162_bits(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u)));
@@ -460,24 +481,40 @@ __device__ __forceinline__ void ring_tile(const Head<D>& hd, uint32_t st, uint32
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt) {
         uint32_t a[4];
-        ldsm_x4_t(a, sv + ring_piece<D>(row, 2 * mt + piece));
-        mma_bf16(S.acc[mt], a, wh[0], wh[1]);
-        mma_bf16(S.acc[mt], a, wl[0], wl[1]);
+        ldsm_x4_t(a, smem_u32(sv) + ring_piece<D>(row, 2 * mt + piece));
+        mma_b16(S.acc[mt], a, wh[0], wh[1]);
+        mma_b16(S.acc[mt], a, wl[0], wl[1]);
     }
 }
 
 template <int D, int KB, int VB, bool LO>
 __global__ void __launch_bounds__(kMaxWarps * 32) sink_decode_kernel(const __grid_constant__ Params p, const __grid_constant__ Args a) {
-    using G = Stage<D, KB, VB>;
+    using G = Buf<D, KB, VB>;
     extern __shared__ __align__(16) unsigned char smem[];
     Head<D>& hd = *reinterpret_cast<Head<D>*>(smem);
     const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int r = lane >> 2, c = lane & 3;
     const int h = blockIdx.y, b = blockIdx.z, rank = blockIdx.x, ctas = gridDim.x;
-    const int stage_bytes = G::bytes(p);
-    const int region = max(kStages * stage_bytes, kPartFloats<D> * 4);
+    const int region = warp_smem<D, KB, VB>(p);
     unsigned char* mine = smem + sizeof(Head<D>) + warp * region;
-    const uint32_t st0 = smem_u32(mine);
+    unsigned char *sk = mine, *sv = mine + G::keys();
+
+    // A negative score scale becomes the query's sign, so that the largest score is the largest product.
+    const float sign = a.scale_log2 < 0.f ? -1.f : 1.f, scale_log2 = fabsf(a.scale_log2);
+
+    // query rows of heads `warp` and `warp + warps`: under way while the length and the page table are read
+    constexpr int C = D / 32;
+    float q[2][C];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        const int x = warp + y * warps;
+        const size_t at = size_t(b) * a.q_stride + size_t(h * p.g + x) * D + lane * C;
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            q[y][i] = x >= p.g ? 0.f
+                      : sign * (a.q_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at + i])
+                                         : static_cast<const float*>(a.q)[at + i]);
+    }
 
     const int L = max(0, min(__ldg(a.lens + b), a.len_cap));
     const int Lq = paged_len(p, 0, L);                    // positions below Lq live in pages, the others in the ring
@@ -499,95 +536,120 @@ __global__ void __launch_bounds__(kMaxWarps * 32) sink_decode_kernel(const __gri
     };
     look_up(0);
 
-    // start the copies of item number k of this warp; what: -1 nothing there, 0 page, else the valid ring slots
-    auto issue = [&](int k, int stage) -> int {
+    // What item number k of this warp is: -1 nothing to do, a page's block below 2^30, or 2^30 + the valid ring slots.
+    constexpr int kIsRing = 1 << 30;
+    auto item = [&](int k) -> int {
         const int it = start + k * step;
-        int what = -1;
         if (k - table_at >= 32) look_up(k);
         const int pg = __shfl_sync(kAll, table, k - table_at);
-        if (it < n_page) {
-            if (pg >= 0) {
-                what = 0;
-                const uint32_t st = st0 + stage * stage_bytes;
-                const size_t blk = size_t(pg) * p.hkv + h;
-                const uint8_t* kc = p.k_codes + blk * G::kK + lane * 16;
-                const uint8_t* vc = p.v_codes + blk * G::kV + lane * 16;
+        if (it < n_page) return pg;
+        if (it >= n_item) return -1;
+        const int slot = (it - n_page) * kRing + (lane & (kRing - 1)), q0 = Lq % p.W;
+        const int x = Lq + (slot >= q0 ? slot - q0 : slot - q0 + p.W);
+        const unsigned any = __ballot_sync(kAll, slot < p.W && visible(x, ns, lo, L)) & 0xffffu;
+        return any ? kIsRing + int(any) : -1;
+    };
+    auto copy_ring = [&](unsigned char* to, const __nv_bfloat16* rows, int k, int what) {
+        const size_t row = (size_t(b) * p.hkv + h) * p.W + (start + k * step - n_page) * kRing;
+        const uint32_t at = smem_u32(to);
+        for (int e = lane; e < kRing * (D / 8); e += 32) {
+            const int i = e / (D / 8), o = e % (D / 8);
+            const bool have = (what >> i) & 1;
+            cp16_zfill(at + ring_piece<D>(i, o), rows + (have ? (row + i) * D + o * 8 : 0), have);
+        }
+    };
+    auto copy_keys = [&](int k, int what) {
+        if (what >= kIsRing) {
+            copy_ring(sk, p.k_win, k, what);
+        } else if (what >= 0) {
+            const uint32_t at = smem_u32(sk);
+            const size_t blk = size_t(what) * p.hkv + h;
+            const uint8_t* kc = p.k_codes + blk * G::kK + lane * 16;
+            if (KB == 1) {                               // rows of D/8 bytes: 8-byte pieces keep the exchange for D = 64
 #pragma unroll
-                for (int e = 0; e < G::kK; e += 512) cp16(st + e + lane * 16, kc + e);
+                for (int t = 0; t < kPage; t += 32)
+                    if (D == 128)
+                        cp16(at + key_slot(lane + t) * 16, kc + t * 16);
+                    else
+                        cp8(at + key_slot(lane + t) * 8, kc - lane * 8 + t * 8);
+            } else {
 #pragma unroll
-                for (int e = 0; e < G::kV; e += 512) cp16(st + G::kK + e + lane * 16, vc + e);
-                const uint8_t* km = reinterpret_cast<const uint8_t*>(p.k_meta) + blk * (kPage * 4) * p.nkg;
-                const uint8_t* vm = reinterpret_cast<const uint8_t*>(p.v_meta) + blk * (kPage * 4) * p.nvg;
-                const uint32_t sm = st + G::kK + G::kV;
-                const int nk = 16 * p.nkg, n = nk + 16 * p.nvg;
-                for (int e = lane; e < n; e += 32) cp16(sm + e * 16, e < nk ? km + e * 16 : vm + (e - nk) * 16);
+                for (int e = 0; e < G::kK / 16; e += 32)   // chunk e / 64, positions e % 64 + lane
+                    cp16(at + ((e & ~63) + key_slot((e & 63) + lane)) * 16, kc + e * 16);
             }
-        } else if (it < n_item) {
-            const int slot = (it - n_page) * kRing + (lane & (kRing - 1)), q0 = Lq % p.W;
-            const int x = Lq + (slot >= q0 ? slot - q0 : slot - q0 + p.W);
-            const bool ok = slot < p.W && visible(x, ns, lo, L);
-            const unsigned any = __ballot_sync(kAll, ok) & 0xffffu;
-            if (any) {
-                what = int(any);
-                const uint32_t st = st0 + stage * stage_bytes;
-                const size_t row = (size_t(b) * p.hkv + h) * p.W + (it - n_page) * kRing;
-                for (int e = lane; e < 2 * kRing * (D / 8); e += 32) {
-                    const int i = e / (D / 8), o = e % (D / 8), sl = i & (kRing - 1);
-                    const bool have = (any >> sl) & 1u;
-                    const __nv_bfloat16* src = (i < kRing ? p.k_win : p.v_win) + (have ? (row + sl) * D + o * 8 : 0);
-                    cp16_zfill(st + (i < kRing ? 0 : kRing * 2 * D) + ring_piece<D>(sl, o), src, have);
+            const uint32_t am = at + G::kK;
+            const uint32_t* km = p.k_meta + blk * kPage * p.nkg;
+            if (D == 128 && p.nkg == 4) {
+#pragma unroll
+                for (int t = lane; t < kPage; t += 32) cp16(am + key_slot(t) * 16, km + t * 4);
+            } else {                                     // one word for every 32 channels
+                const int sh = __ffs(G::kUnits / p.nkg) - 1;
+                for (int e = lane; e < kPage * G::kUnits; e += 32) {
+                    const int t = e / G::kUnits, u = e % G::kUnits;
+                    cp4(am + (key_slot(t) * G::kUnits + u) * 4, km + t * p.nkg + (u >> sh));
                 }
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        return what;
     };
-    int what[kStages];
+    const int vlog = __ffs(p.nvg) - 1;
+    auto copy_values = [&](int k, int what) {
+        if (what >= kIsRing) {
+            copy_ring(sv, p.v_win, k, what);
+        } else if (what >= 0) {
+            const uint32_t at = smem_u32(sv);
+            const size_t blk = size_t(what) * p.hkv + h;
+            const uint8_t* vc = p.v_codes + blk * G::kV + lane * 16;
 #pragma unroll
-    for (int k = 0; k < kStages; ++k) what[k] = issue(k, k);
-
-    // ---- queries: each head's row by one warp ----
-    {
-        constexpr int C = D / 32;
-        const int g = p.g;
-        for (int x = warp; x < kHeads; x += warps) {
-            float q[C];
-#pragma unroll
-            for (int i = 0; i < C; ++i) q[i] = 0.f;
-            if (x < g) {
-                const size_t at = size_t(b) * a.q_stride + size_t(h * g + x) * D + lane * C;
-#pragma unroll
-                for (int i = 0; i < C; ++i)
-                    q[i] = a.q_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at + i])
-                                    : static_cast<const float*>(a.q)[at + i];
+            for (int e = 0; e < G::kV; e += 512) cp16(at + e + lane * 16, vc + e);
+            const uint32_t* vm = p.v_meta + blk * kPage * p.nvg;
+            if (p.nvg == 1) {
+                if (lane < 16) cp16(at + G::kV + lane * 16, vm + lane * 4);
+            } else {                                     // group-major
+                for (int e = lane; e < kPage * p.nvg; e += 32) {
+                    const int t = e >> vlog, g = e & (p.nvg - 1);
+                    cp4(at + G::kV + (g * kPage + t) * 4, vm + e);
+                }
             }
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-                const __nv_bfloat16 hi = __float2bfloat16_rn(q[i]);
-                hd.bh[x][lane * C + i] = hi;
-                hd.bl[x][lane * C + i] = __float2bfloat16_rn(q[i] - __bfloat162float(hi));
-            }
-            if (p.rotate) rotate_warp<D>(q, p.signs, lane);
-            float m = 0.f, sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < C; ++i) m = fmaxf(m, fabsf(q[i]));
-            for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, w));
-            // a power of two that brings the head's largest element into [2^7, 2^8)
-            const int ex = max(-100, int(__float_as_uint(m) >> 23) - 127);
-            const float up = __uint_as_float(uint32_t(127 + 7 - ex) << 23);
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-                const float v = q[i] * up;
-                const __half hi = __float2half_rn(v);
-                hd.qh[x][lane * C + i] = hi;
-                hd.ql[x][lane * C + i] = __float2half_rn(v - __half2float(hi));
-                sum += v;
-            }
-#pragma unroll
-            for (int w = 1; w < 32 / C; w <<= 1) sum += __shfl_xor_sync(kAll, sum, w);
-            if (lane % (32 / C) == 0) hd.qsum[x][lane / (32 / C)] = sum;
-            if (lane == 0) hd.factor[x] = a.scale_log2 * __uint_as_float(uint32_t(127 - 7 + ex) << 23);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int now = item(0);
+    copy_keys(0, now);
+    copy_values(0, now);
+
+    // ---- queries to shared memory, a head's row by one warp ----
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        const int x = warp + y * warps;
+        if (x >= kHeads) break;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const __nv_bfloat16 hi = __float2bfloat16_rn(q[y][i]);
+            hd.bh[x][lane * C + i] = hi;
+            hd.bl[x][lane * C + i] = __float2bfloat16_rn(q[y][i] - __bfloat162float(hi));
+        }
+        if (p.rotate) rotate_warp<D>(q[y], p.signs, lane);
+        float m = 0.f, sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) m = fmaxf(m, fabsf(q[y][i]));
+        m = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(m)));
+        // a power of two that brings the head's largest element into [2^7, 2^8)
+        const int ex = max(-100, int(__float_as_uint(m) >> 23) - 127);
+        const float up = __uint_as_float(uint32_t(127 + 7 - ex) << 23);
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const float v = q[y][i] * up;
+            const __half hi = __float2half_rn(v);
+            hd.qh[x][lane * C + i] = hi;
+            hd.ql[x][lane * C + i] = __float2half_rn(v - __half2float(hi));
+            sum += v;
+        }
+#pragma unroll
+        for (int w = 1; w < 32 / C; w <<= 1) sum += __shfl_xor_sync(kAll, sum, w);
+        if (lane % (32 / C) == 0) hd.qsum[x][lane / (32 / C)] = sum;
+        // (never zero: -inf times it has to stay -inf)
+        if (lane == 0) hd.factor[x] = fmaxf(scale_log2 * __uint_as_float(uint32_t(127 - 7 + ex) << 23), 1e-37f);
     }
     __syncthreads();
     uint32_t qh[D / 8], ql[LO ? D / 8 : 1];
@@ -622,39 +684,39 @@ __global__ void __launch_bounds__(kMaxWarps * 32) sink_decode_kernel(const __gri
     S.ref[0] = S.ref[1] = kRefNone;
 
     for (int k = 0; start + k * step < n_item; ++k) {
-        const int it = start + k * step, stage = k % kStages;
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        const int next = item(k + 1);
+        const bool page = now >= 0 && now < kIsRing;
+        const int base = page ? logical(start + k * step) * kPage : 0;
+        const bool edge = base + kPage > Lq || (base < lo && base + kPage > ns);
+        float s[8][2];
+        asm volatile("cp.async.wait_group 1;" ::: "memory");   // the keys are here, the values may not be
         __syncwarp();
-        int now = what[0];
-#pragma unroll
-        for (int i = 1; i < kStages; ++i)
-            if (stage == i) now = what[i];
-        const uint32_t st = st0 + stage * stage_bytes;
-        if (now >= 0) {
-            if (it < n_page) {
-                const int base = logical(it) * kPage;
-                const bool edge = base + kPage > Lq || (base < lo && base + kPage > ns);
-                page_tile<D, KB, VB, LO>(p, st, base, ns, lo, Lq, edge, qh, ql, qz, factor, S);
-            } else {
-                ring_tile<D>(hd, st, uint32_t(now), ring_lo, a.scale_log2, S);
-            }
-        }
+        if (page)
+            page_scores<D, KB, VB, LO>(p, sk, base, ns, lo, Lq, edge, qh, ql, qz, s);
+        else if (now >= kIsRing)
+            ring_scores<D>(hd, sk, uint32_t(now), ring_lo, scale_log2, s);
         __syncwarp();
-        const int next = issue(k + kStages, stage);
-#pragma unroll
-        for (int i = 0; i < kStages; ++i)
-            if (stage == i) what[i] = next;
+        copy_keys(k + 1, next);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+        if (page)
+            page_values<D, KB, VB>(p, sv, base, ns, lo, Lq, edge, s, factor, S);
+        else if (now >= kIsRing)
+            ring_values<D>(sv, s, S);
+        __syncwarp();
+        copy_values(k + 1, next);
+        now = next;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
 
-    // ---- this warp's sums to its part of shared memory (its stages are free) ----
+    // ---- this warp's sums to its part of shared memory (its buffers are free) ----
     float* part = reinterpret_cast<float*>(mine);
     S.l[0] = sum_rows(S.l[0]);
     S.l[1] = sum_rows(S.l[1]);
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt) {
-        const int gi = 16 * mt / p.vg;                   // all 16 channels of a tile are in one group
+        const int gi = 16 * mt >> (__ffs(p.vg) - 1);     // all 16 channels of a tile are in one group
         const float z0 = __shfl_sync(kAll, S.zero[0], 4 * gi + c), z1 = __shfl_sync(kAll, S.zero[1], 4 * gi + c);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -667,39 +729,94 @@ __global__ void __launch_bounds__(kMaxWarps * 32) sink_decode_kernel(const __gri
         part[kHeads * D + kHeads + 2 * c + 1] = S.l[1];
     }
 
-    // ---- all parts of the cluster: each CTA finishes its share of the outputs ----
+    // ---- the CTA's sums: weights of its warps' parts, then one part for the CTA in place of warp 0's ----
+    __syncthreads();
+    const auto parts = [&](int w) { return reinterpret_cast<float*>(smem + sizeof(Head<D>) + w * region); };
+    float* weight = reinterpret_cast<float*>(&hd.qh[0][0]);   // [warp][head]; the queries are in registers by now
+    if (warp < kHeads / 4) {
+        const int x = 4 * warp + r % 4;                       // lanes of one head: c + 4 * (r / 4), warps in steps of 8
+        float top = kRefNone, l = 0.f;
+        const int w0 = c + 4 * (r >> 2);
+        float ref[2], sum[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int w = w0 + 8 * i;
+            ref[i] = w < warps ? parts(w)[kHeads * D + x] : kRefNone;
+            sum[i] = w < warps ? parts(w)[kHeads * D + kHeads + x] : 0.f;
+            top = fmaxf(top, ref[i]);
+        }
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 16));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float f = ex2(ref[i] - top);
+            weight[(w0 + 8 * i) * kHeads + x] = f;
+            l = fmaf(sum[i], f, l);
+        }
+        l += __shfl_xor_sync(kAll, l, 1);
+        l += __shfl_xor_sync(kAll, l, 2);
+        l += __shfl_xor_sync(kAll, l, 16);
+        if (w0 == 0) {
+            hd.factor[x] = top;
+            hd.qsum[x][0] = l;
+        }
+    }
+    __syncthreads();
     namespace cg = cooperative_groups;
     cg::cluster_group cl = cg::this_cluster();
-    if (ctas > 1)
-        cl.sync();
-    else
-        __syncthreads();
-    for (int e = rank * blockDim.x + threadIdx.x; e < p.g * (D / 2); e += ctas * blockDim.x) {
-        const int x = e / (D / 2), j = 2 * (e % (D / 2));
-        float top = kRefNone;
-        for (int i = 0; i < ctas; ++i) {
-            const unsigned char* base = ctas > 1 ? cl.map_shared_rank(smem, i) : smem;
-            for (int w = 0; w < warps; ++w)
-                top = fmaxf(top, reinterpret_cast<const float*>(base + sizeof(Head<D>) + w * region)[kHeads * D + x]);
+    for (int e = threadIdx.x; e < p.g * (D / 2); e += blockDim.x) {
+        const int x = e / (D / 2);
+        float2 o = make_float2(0.f, 0.f);
+#pragma unroll 4
+        for (int w = 0; w < warps; ++w) {
+            const float2 v = reinterpret_cast<const float2*>(parts(w))[e];
+            const float f = weight[w * kHeads + x];
+            o.x = fmaf(v.x, f, o.x);
+            o.y = fmaf(v.y, f, o.y);
         }
-        float o0 = 0.f, o1 = 0.f, l = 0.f;
-        for (int i = 0; i < ctas; ++i) {
-            const unsigned char* base = ctas > 1 ? cl.map_shared_rank(smem, i) : smem;
-            for (int w = 0; w < warps; ++w) {
-                const float* q = reinterpret_cast<const float*>(base + sizeof(Head<D>) + w * region);
-                const float f = ex2(q[kHeads * D + x] - top);
-                const float2 v = *reinterpret_cast<const float2*>(q + x * D + j);
-                o0 = fmaf(v.x, f, o0);
-                o1 = fmaf(v.y, f, o1);
-                l = fmaf(q[kHeads * D + kHeads + x], f, l);
-            }
+        if (ctas > 1) {
+            reinterpret_cast<float2*>(parts(0))[e] = o;
+        } else {
+            const float l = hd.qsum[x][0], inv = l > 0.f ? 1.f / l : 0.f;
+            const size_t row = size_t(b) * p.hq + h * p.g + x;
+            reinterpret_cast<__nv_bfloat162*>(a.out + row * D)[e % (D / 2)] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+            if (a.lse && e % (D / 2) == 0)
+                a.lse[row] = l > 0.f ? (hd.factor[x] + log2f(l)) * 0.693147180559945309f : -INFINITY;
+        }
+    }
+    if (ctas == 1) return;
+    // ---- the cluster's sums: each CTA finishes its share of the outputs ----
+    cl.sync();
+    for (int e = rank * blockDim.x + threadIdx.x; e < p.g * (D / 2); e += ctas * blockDim.x) {
+        const int x = e / (D / 2);
+        float ref[8], sum[8];
+        float2 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const unsigned char* at = cl.map_shared_rank(smem, i < ctas ? i : 0);
+            const Head<D>& other = *reinterpret_cast<const Head<D>*>(at);
+            ref[i] = i < ctas ? other.factor[x] : kRefNone;
+            sum[i] = i < ctas ? other.qsum[x][0] : 0.f;
+            v[i] = i < ctas ? reinterpret_cast<const float2*>(at + sizeof(Head<D>))[e] : make_float2(0.f, 0.f);
+        }
+        float top = ref[0], l = 0.f;
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top = fmaxf(top, ref[i]);
+        float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float f = ex2(ref[i] - top);
+            l = fmaf(sum[i], f, l);
+            o.x = fmaf(v[i].x, f, o.x);
+            o.y = fmaf(v[i].y, f, o.y);
         }
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const size_t row = size_t(b) * p.hq + h * p.g + x;
-        *reinterpret_cast<__nv_bfloat162*>(a.out + row * D + j) = __floats2bfloat162_rn(o0 * inv, o1 * inv);
-        if (a.lse && j == 0) a.lse[row] = l > 0.f ? (top + log2f(l)) * 0.693147180559945309f : -INFINITY;
+        reinterpret_cast<__nv_bfloat162*>(a.out + row * D)[e % (D / 2)] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+        if (a.lse && e % (D / 2) == 0) a.lse[row] = l > 0.f ? (top + log2f(l)) * 0.693147180559945309f : -INFINITY;
     }
-    if (ctas > 1) cl.sync();                             // no CTA leaves while another reads its part
+    cl.sync();                                           // no CTA leaves while another reads its part
 }
 
 // ---------------------------------------------------------------- launch
@@ -733,11 +850,17 @@ cudaError_t launch_decode_one(const Params& p, const Args& a, int sms, cudaStrea
         if (e != cudaSuccess) return e;
         opted[dev] = kMost;
     }
-    // four warps, or two where the stages of 8-bit codes would leave room for one CTA only
-    int warps = 4;
-    if (2 * decode_smem<D, KB, VB>(p, 4) > kMost) warps = 2;
+    // four warps a CTA, or as many up to eight as bring the most warps onto an SM (large buffers)
+    int warps = 4, per_sm = 1;
+    for (int w = 4, most = 0; w <= 8; ++w) {
+        const int n = std::min(kMaxWarps / w, (228 * 1024) / (decode_smem<D, KB, VB>(p, w) + 1024));
+        if (n * w > most) {
+            most = n * w;
+            warps = w;
+            per_sm = n;
+        }
+    }
     const int smem = decode_smem<D, KB, VB>(p, warps);
-    const int per_sm = std::max(1, std::min(12 / warps, (228 * 1024) / (smem + 1024)));
     const long long bound = std::min<long long>(a.len_cap, (long long)a.sinks + a.span + 2 * kPage);
     const int items = int((bound + kPage - 1) / kPage) + (std::min(p.W, a.len_cap) + kRing - 1) / kRing;
     const int n = split_ctas((long long)p.batch * p.hkv, items, warps, sms * per_sm);
