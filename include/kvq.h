@@ -364,11 +364,16 @@ int kvq_dequantize(const kvq_layout* layout, const kvq_cache* cache,
  *    joint projection can be passed as they lie); q 16-byte aligned.
  *  - out is bf16, rows [Hq][d] without gaps, 16-byte aligned; lse fp32 rows
  *    [Hq] (natural log) or NULL.
- *  - Scores, softmax statistics and sums are fp32; attention weights and
- *    reconstructed keys and values are rounded to fp16 at the tensor cores,
- *    so reconstructed values must lie within +-65504.  out is within 1e-3 +
- *    1e-3*|o| + bf16 rounding of the same sum in fp64, lse within 1e-3 +
- *    1e-3*|lse|, for normal inputs (rows of unit-scale scores).
+ *  - Scores, softmax statistics and sums are fp32; out is rounded to bf16
+ *    once.  Single tokens over key groups of 32 channels or more multiply the
+ *    codes themselves: out is within 1e-3 + 1e-3*|o| (+ its rounding) and lse
+ *    within 1e-3 + 1e-3*|lse| of the same sums in fp64.  Chunks, and single
+ *    tokens of the other layouts, round keys, values and weights to fp16 (and
+ *    queries that are fp32 or rotated), each by up to 2^-11 of itself: a score
+ *    is off by at most D = 2^-11 sum_j |q_j k_j| * |sm_scale| (twice that with
+ *    the query's rounding), lse by D, out by a factor within exp(+-2D) of each
+ *    weight and 2^-10 of sum a |v|.  There reconstructed keys and values must
+ *    lie within +-65504.
  *  - No workspace; calls on different streams may overlap as long as no
  *    call writes the cache.  Results do not depend on what else runs. */
 

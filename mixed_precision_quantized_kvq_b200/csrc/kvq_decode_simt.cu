@@ -440,6 +440,8 @@ unsigned* status_ptr() {
 }
 }  // namespace
 
+unsigned* status_words() { return status_ptr(); }
+
 cudaError_t decode_status(unsigned* wait_timeouts, unsigned* bad_tickets, bool clear) {
     unsigned v[2] = {0u, 0u};
     cudaError_t e = cudaMemcpyFromSymbol(v, g_decode_status, sizeof(v));

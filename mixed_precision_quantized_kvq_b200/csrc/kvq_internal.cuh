@@ -184,5 +184,7 @@ cudaError_t launch_decode(const Params& p, const void* q, int q_bf16, const int3
 // waits that expired, [1] tickets found above their count.  Read and
 // optionally cleared by decode_status (blocking).
 cudaError_t decode_status(unsigned* wait_timeouts, unsigned* bad_tickets, bool clear);
+// the device words themselves on the current device (null when they cannot be found)
+unsigned* status_words();
 
 }  // namespace kvq

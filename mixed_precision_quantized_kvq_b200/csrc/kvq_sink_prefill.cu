@@ -1,0 +1,751 @@
+// Attention of a chunk of new queries with sinks and a sliding span over the
+// quantized cache (kvq_sink_prefill_attention) on the 5th-generation tensor
+// cores (tcgen05, sm_100a).  Every layout; also the single-token form of the
+// layouts whose scales are not shared by 32 channels (kvq_sink_decode.cuh).
+//
+//     S = Q K^T,  P = 2^(factor S - ref) where visible,  O += P V,  l += P 1
+//
+// over tiles of 128 positions (two pages), with a running reference exponent
+// per query row; O / l is rounded to bf16.  Bound by the tensor cores and the
+// exponentials (one per visible pair: 16 a clock and SM, which takes as long as
+// the two products at head_dim 128).
+//
+// One CTA per SM takes 256 rows of one (sequence, kv-head): two blocks of 128,
+// each 128/g queries with their g heads.  Reconstructing a key or value costs
+// about two issue slots an element, so a tile is reconstructed once, to fp16,
+// for both blocks, and while one block's exponentials run the tensor cores
+// work on the other block.  Warps:
+//   0-3, 4-7   weights of block 0 and 1: thread = row.  S from tensor memory
+//              twice (maximum, then weights), P back over S as fp16.  O is
+//              rescaled only when a row's maximum has grown by more than 2^8.
+//   8-11       reconstruct: thread = position for keys, channel for values
+//              (keys with groups along positions: thread = two channels).
+//   12         issues the products.
+// Operands are 8x16-byte core matrices without swizzle, all 16-byte pieces of
+// the same eight columns together, which makes the writers' 16-byte stores
+// contiguous over a warp.  A word holds the codes (i, i + n/2) in the same
+// bits of its halves, so reconstructed pairs come out in that order; instead of
+// sorting them, the query's channels are stored in the same order (keys), and
+// key rows, that is, the columns of S and P (values).
+#include <math.h>
+
+#include "kvq_sink.cuh"
+#include "kvq_tc_ptx.cuh"
+
+namespace kvq {
+namespace sink {
+namespace {
+
+using namespace ptx;
+
+constexpr int kRows = 128;                    // rows of a block
+constexpr int kTile = 128;                    // positions of a tile
+constexpr int kThreads = 13 * 32;
+constexpr int kStages = 2;
+constexpr uint64_t kLimitNs = 2000000000ull;  // a wait that takes longer gives up
+constexpr float kRefNone = -1e30f;
+constexpr int kKeyPitch = kTile * 16 + 16;    // bytes between 16-byte columns of the key tile: the extra piece puts
+                                              // neighbouring columns in different banks (keys by channel pairs)
+
+// positions of the halves of pair p in a run of words of N codes
+template <int N>
+__device__ __forceinline__ constexpr int pair_low(int p) { return p / (N / 2) * N + p % (N / 2); }
+// where code i of a run lies once the words are unpacked, and back
+__device__ __forceinline__ int slot_of(int i, int n) { return (i & ~(n - 1)) + 2 * (i & (n / 2 - 1)) + ((i & (n / 2)) ? 1 : 0); }
+__device__ __forceinline__ int code_of(int s, int n) { return (s & ~(n - 1)) + ((s & (n - 1)) >> 1) + ((s & 1) ? n / 2 : 0); }
+
+template <int D>
+struct Smem {
+    static constexpr int kQ = D / 8 * kRows * 16;       // one block's queries
+    static constexpr int kK = D / 8 * kKeyPitch;
+    static constexpr int kV = kTile / 8 * D * 16;
+    unsigned char q[2][kQ];
+    unsigned char k[kStages][(kK + 127) / 128 * 128];
+    unsigned char v[kStages][kV];
+    uint32_t vscale[8][kTile / 2];                      // value scales and zero points of pairs, by group
+    uint32_t vzero[8][kTile / 2];
+    float factor[2][kRows];
+    uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages], sfull[2], pfull[2];
+    uint32_t tmem;
+    int hidden[4];                                      // tile j % 4: bit i set when page i is absent
+    int failed;
+};
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(0), "r"(0), "r"(0), "r"(0)
+        : "memory");
+}
+// instruction descriptor: fp16 A and B (K-major), fp32 accumulator
+constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24); }
+
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_cast<__half2*>(&w); }
+// fp16 range, so that one element out of it does not turn a row into NaN
+__device__ __forceinline__ __half to_half(float x) { return __float2half_rn(fminf(fmaxf(x, -65504.f), 65504.f)); }
+
+// The 16/BITS pairs of a word as exact fp16 numbers.  With 0x6400 above them the ten low bits of a half-word are the
+// mantissa of 1024 + code * 2^position; one exact operation takes both away.
+template <int BITS>
+__device__ __forceinline__ void unpack(uint32_t w, __half2 (&c)[16 / BITS]) {
+    constexpr int kSpan = 10 / BITS * BITS < 10 ? (BITS == 4 ? 8 : 8) : 10;
+    constexpr uint32_t kMask = ((1u << BITS) - 1u) * 0x00010001u;
+#pragma unroll
+    for (int i = 0; i < 16 / BITS; ++i) {
+        const int at = i * BITS % kSpan, shift = i * BITS - at;
+        const __half2 x = half2_of(((w >> shift) & (kMask << at)) | 0x64006400u);
+        if (at == 0)
+            c[i] = __hsub2(x, half2_of(0x64006400u));
+        else
+            c[i] = __hfma2(x, half2_of(uint32_t(15 - at) * 0x04000400u), half2_of(0x80008000u | uint32_t(25 - at) * 0x04000400u));
+    }
+}
+
+// the lowest n bits, for any n
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+// scores of 32 columns whose positions are not in `seen`: minus infinity
+template <int N>
+__device__ __forceinline__ void hide(uint32_t (&s)[32], uint32_t seen) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const int o = (i & ~(N - 1)) + ((i & (N - 1)) >> 1) + ((i & 1) ? N / 2 : 0);
+        if (!(seen & (1u << o))) s[i] = 0xff800000u;
+    }
+}
+
+// What a CTA works on.
+struct Work {
+    int b, h, L, Lq, lo, p_max, sinks;          // lo: first position of the first query's span
+    int n_sink, first, n_tile;                  // tiles of the sinks, first tile of the span, all tiles
+    __device__ __forceinline__ int tile_start(int j) const { return (j < n_sink ? j : j - n_sink + first) * kTile; }
+    // seen by some row (a necessary condition; the rows' own masks are exact)
+    __device__ __forceinline__ bool used(int x) const { return x <= p_max && (x < sinks || x >= lo); }
+};
+
+// One row of D channels by D/8 neighbouring lanes, eight channels each, to column `row` of an operand of fp16 pieces
+// `pitch` bytes apart; n: codes per word of the keys (channel order).  scaled: by a power of two into [2^13, 2^14);
+// returns that power's inverse.  The whole warp calls it; nothing is stored where `to` is null.
+template <int D>
+__device__ __forceinline__ float put_row(float (&x)[8], const int8_t* signs, bool scaled, unsigned char* to, int pitch, int row,
+                                         int n) {
+    const int oct = threadIdx.x % (D / 8);
+    if (signs) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= float(__ldg(signs + oct * 8 + i));
+#pragma unroll
+        for (int s = 1; s < 8; s <<= 1)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (!(i & s)) {
+                    const float u = x[i], w = x[i + s];
+                    x[i] = u + w;
+                    x[i + s] = u - w;
+                }
+#pragma unroll
+        for (int m = 1; m < D / 8; m <<= 1)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float o = __shfl_xor_sync(0xffffffffu, x[i], m);
+                x[i] = (oct & m) ? o - x[i] : x[i] + o;
+            }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= RotScale<D>::v;
+    }
+    float up = 1.f, down = 1.f;
+    if (scaled) {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+#pragma unroll
+        for (int w = 1; w < D / 8; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+        const int e = max(-100, int(__float_as_uint(m) >> 23) - 127);
+        up = __uint_as_float(uint32_t(127 + 13 - e) << 23);
+        down = __uint_as_float(uint32_t(127 - 13 + e) << 23);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int s = slot_of(oct * 8 + i, n);
+        if (to) *reinterpret_cast<__half*>(to + (s >> 3) * pitch + row * 16 + (s & 7) * 2) = to_half(x[i] * up);
+    }
+    return down;
+}
+
+__device__ __forceinline__ void load8(const void* src, bool bf16, size_t at, float (&x)[8]) {
+    if (bf16) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(src) + at));
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(u[i] << 16);
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    } else {
+        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
+        const float4 a = __ldg(f), b = __ldg(f + 1);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+}
+
+// ---------------------------------------------------------------- keys
+
+// one position's codes (words in `raw`) with their metadata, to row `row` of the key tile
+template <int BITS, int D>
+__device__ __forceinline__ void put_key(const Params& p, const uint4 (&raw)[8], const uint32_t* meta, unsigned char* to, int row) {
+    constexpr int N = 32 / BITS, W = D / N;              // codes a word, words a row
+    const int kshift = __ffs(p.kg) - 1;
+    __half2 out[4];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const uint4& q = raw[w / 4];
+        const uint32_t word = w % 4 == 0 ? q.x : w % 4 == 1 ? q.y : w % 4 == 2 ? q.z : q.w;
+        const uint32_t m0 = __ldg(meta + (w * N >> kshift)), m1 = N > 16 ? __ldg(meta + ((w * N + N / 2) >> kshift)) : m0;
+        const __half2 scale = half2_of(__byte_perm(m0, m1, 0x5410)), zero = half2_of(__byte_perm(m0, m1, 0x7632));
+        __half2 c[N / 2];
+        unpack<BITS>(word, c);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const int s = w * (N / 2) + i;               // pair of the row
+            out[s & 3] = __hfma2(c[i], scale, zero);
+            if ((s & 3) == 3)
+                *reinterpret_cast<uint4*>(to + (s >> 2) * kKeyPitch + row * 16) =
+                    make_uint4(bits(out[0]), bits(out[1]), bits(out[2]), bits(out[3]));
+        }
+    }
+}
+
+// keys with groups along positions: the codes of channels 2*cp and 2*cp + 1 of one page, to rows of the key tile
+template <int BITS, int D>
+__device__ __forceinline__ void put_key_pairs(const Params& p, const uint4 (&raw)[8], const uint32_t* meta, int cp, int page,
+                                              int x0, int Lq, int vn, unsigned char* to) {
+    constexpr int N = 32 / BITS, W = kPage / N;          // codes a word, words a run
+    constexpr int H = (W + 3) / 4;                       // 16-byte pieces a run
+    const int kshift = __ffs(p.kg) - 1;
+    unsigned char* col = to + (cp >> 2) * kKeyPitch + (cp & 3) * 4;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const uint4 &a = raw[w / 4], &b = raw[H + w / 4];
+        const uint32_t wa = w % 4 == 0 ? a.x : w % 4 == 1 ? a.y : w % 4 == 2 ? a.z : a.w;
+        const uint32_t wb = w % 4 == 0 ? b.x : w % 4 == 1 ? b.y : w % 4 == 2 ? b.z : b.w;
+        __half2 ca[N / 2], cb[N / 2];
+        unpack<BITS>(wa, ca);
+        unpack<BITS>(wb, cb);
+        __half2 scale[2], zero[2];                       // of the words' low and high codes' groups
+#pragma unroll
+        for (int e = 0; e < (N > 16 ? 2 : 1); ++e) {
+            const uint2 m = __ldg(reinterpret_cast<const uint2*>(meta + size_t((w * N + e * (N / 2)) >> kshift) * D + 2 * cp));
+            scale[e] = half2_of(__byte_perm(m.x, m.y, 0x5410));
+            zero[e] = half2_of(__byte_perm(m.x, m.y, 0x7632));
+        }
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = w * N + i + e * (N / 2);
+                const __half2 c = half2_of(__byte_perm(bits(ca[i]), bits(cb[i]), e ? 0x7632 : 0x5410));
+                const __half2 k = __hfma2(c, scale[N > 16 ? e : 0], zero[N > 16 ? e : 0]);
+                if (x0 + t < Lq) *reinterpret_cast<uint32_t*>(col + slot_of(page * kPage + t, vn) * 16) = bits(k);
+            }
+    }
+}
+
+// ---------------------------------------------------------------- values
+
+// one channel's run of a page to the value tile: pieces of eight slots, D*16 bytes apart
+template <int BITS, int D>
+__device__ __forceinline__ void put_value(const Smem<D>& sm, const uint4 (&raw)[4], int group, int page, unsigned char* to) {
+    constexpr int N = 32 / BITS, W = kPage / N;
+    const uint4* scale = reinterpret_cast<const uint4*>(&sm.vscale[group][page * (kPage / 2)]);
+    const uint4* zero = reinterpret_cast<const uint4*>(&sm.vzero[group][page * (kPage / 2)]);
+    __half2 out[4];
+    uint4 s4, z4;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const uint4& q = raw[w / 4];
+        const uint32_t word = w % 4 == 0 ? q.x : w % 4 == 1 ? q.y : w % 4 == 2 ? q.z : q.w;
+        __half2 c[N / 2];
+        unpack<BITS>(word, c);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const int s = w * (N / 2) + i;               // pair of the run
+            if ((s & 3) == 0) {
+                s4 = scale[s >> 2];
+                z4 = zero[s >> 2];
+            }
+            const uint32_t sc = (s & 3) == 0 ? s4.x : (s & 3) == 1 ? s4.y : (s & 3) == 2 ? s4.z : s4.w;
+            const uint32_t ze = (s & 3) == 0 ? z4.x : (s & 3) == 1 ? z4.y : (s & 3) == 2 ? z4.z : z4.w;
+            out[s & 3] = __hfma2(c[i], half2_of(sc), half2_of(ze));
+            if ((s & 3) == 3)
+                *reinterpret_cast<uint4*>(to + ((s >> 2) + page * (kPage / 8)) * (D * 16)) =
+                    make_uint4(bits(out[0]), bits(out[1]), bits(out[2]), bits(out[3]));
+        }
+    }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_constant__ Params p,
+                                                                   const __grid_constant__ Args a, unsigned* status) {
+    extern __shared__ unsigned char raw_smem[];
+    Smem<D>& sm = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw_smem) + 127) & ~uintptr_t(127));
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    Work wk;
+    wk.b = blockIdx.z;
+    wk.h = blockIdx.y;
+    Seq sq;
+    if (!sequence(a, wk.b, sq)) return;
+    const int g = p.g, QT = kRows / g;                    // queries of a block
+    const int i0 = int(gridDim.x - 1 - blockIdx.x) * 2 * QT;   // the last queries see the most: first
+    if (i0 >= sq.n) return;
+    const int nq = min(2 * QT, sq.n - i0);
+    const bool two = nq > QT;
+    wk.L = sq.L;
+    wk.Lq = paged_len(p, a.kpc, sq.L);
+    wk.p_max = sq.base + i0 + nq - 1;
+    wk.lo = span_begin(sq.base + i0, a.span);
+    wk.sinks = a.sinks;
+    // an empty sequence (decode) has no position at all
+    wk.n_sink = (min(a.sinks, min(wk.lo, wk.p_max + 1)) + kTile - 1) / kTile;
+    wk.first = max(wk.n_sink, wk.lo / kTile);
+    wk.n_tile = wk.n_sink + max(0, (wk.p_max + kTile) / kTile - wk.first);
+    const int kn = a.kpc ? 2 : 32 / p.kb, vn = 32 / p.vb; // order of the key's channels (2: as they are) and of positions
+
+    // ---- set up ----
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sm.kfull[i], 128);
+            mbar_init(&sm.vfull[i], 128);
+            mbar_init(&sm.kempty[i], 1);
+            mbar_init(&sm.vempty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.sfull[i], 1);
+            mbar_init(&sm.pfull[i], 128);
+        }
+        sm.failed = 0;
+        mbar_fence_init();
+    }
+    if (warp == 12) {
+        tmem_alloc(&sm.tmem, 512);
+        tmem_relinquish();
+    }
+    {   // queries, two (or four) rows a warp at a time
+        constexpr int kPer = 32 / (D / 8);
+        const float scale = fabsf(a.scale_log2), sign = a.scale_log2 < 0.f ? -1.f : 1.f;
+        for (int r0 = warp * kPer; r0 < 2 * kRows; r0 += kThreads / 32 * kPer) {
+            const int rr = r0 + lane / (D / 8), m = rr / kRows, r = rr % kRows;
+            const int qi = m * QT + r / g, oct = lane % (D / 8);
+            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (r < QT * g && qi < nq)
+                load8(a.q, a.q_bf16, (sq.row + i0 + qi) * a.q_stride + size_t(wk.h * g + r % g) * D + oct * 8, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] *= sign;
+            const float down = put_row<D>(x, p.rotate ? p.signs : nullptr, true, sm.q[m], kRows * 16, r, kn);
+            // (never zero: -inf times it has to stay -inf)
+            if (oct == 0) sm.factor[m][r] = fmaxf(scale * down, 1e-37f);
+        }
+    }
+    fence_proxy_async();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;                        // S0 S1 O0 O1, 128 (D) columns each
+
+    // a wait that gives up is remembered: every role stops at its next one.  The answer is the warp's.
+    auto wait = [&](uint64_t* bar, int parity) -> bool {
+        bool done = !*reinterpret_cast<volatile int*>(&sm.failed) && mbar_wait(bar, uint32_t(parity), kLimitNs);
+        done = __all_sync(0xffffffffu, done);
+        if (!done && lane == 0 && atomicExch(&sm.failed, 1) == 0) atomicAdd(status, 1u);
+        return done;
+    };
+
+    if (warp < 8) {
+        // ------------------------------------------------ weights
+        const int m = warp >> 2, r = threadIdx.x & 127;
+        if (m == 0 || two) {
+            const uint32_t lanes = uint32_t(warp & 3) * 32u << 16;
+            const uint32_t ts = tmem + m * 128 + lanes, to = tmem + 256 + m * D + lanes;
+            const float factor = sm.factor[m][r];
+            const int q_in = r / g;
+            const int t = sq.base + i0 + m * QT + min(q_in, QT - 1);
+            const int t_first = sq.base + i0 + m * QT, t_last = min(t_first + QT - 1, wk.p_max);
+            float ref = kRefNone, l = 0.f;
+            bool ok = true;
+            for (int j = 0; j < wk.n_tile && ok; ++j) {
+                ok = wait(&sm.sfull[m], j & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const int t0 = wk.tile_start(j), hidden = *reinterpret_cast<volatile int*>(&sm.hidden[j & 3]);
+                // every row of the block sees the whole tile?
+                const bool whole = !hidden && t0 + kTile - 1 <= t_first && (t_last - t0 < a.span || t0 + kTile <= a.sinks);
+                uint32_t s[32];
+                // bit o: position t0 + 32*c + o is visible to this row
+                auto seen = [&](int c) -> uint32_t {
+                    const int x = t0 + 32 * c;
+                    uint32_t v = below(t - x + 1) & (~below(max(t - a.span, -1) - x + 1) | below(a.sinks - x));
+                    if ((hidden >> (c >> 1)) & 1) v &= ~below(wk.Lq - x);
+                    return v;
+                };
+                auto mask = [&](int c) {
+                    const uint32_t v = seen(c);
+                    if (vn == 16) hide<16>(s, v);
+                    if (vn == 8) hide<8>(s, v);
+                    if (vn == 4) hide<4>(s, v);
+                    if (vn == 32) hide<32>(s, v);
+                };
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld32(ts + c * 32, s);
+                    tc_wait_ld();
+                    if (!whole) mask(c);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+                }
+                const float need = mx * factor;
+                if (__any_sync(0xffffffffu, need > ref + 8.f)) {
+                    const float up = fmaxf(ref, need), f = ex2(ref - up);
+                    ref = up;
+                    l *= f;
+                    if (j > 0) {                          // the product with the last tile's values is done: S came after it
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            tmem_ld32(to + c * 32, s);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * f);
+                            tmem_st32(to + c * 32, s);
+                        }
+                        tc_wait_st();
+                    }
+                }
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld32(ts + c * 32, s);
+                    tc_wait_ld();
+                    if (!whole) mask(c);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float x = ex2(fmaf(__uint_as_float(s[2 * i]), factor, -ref));
+                        const float y = ex2(fmaf(__uint_as_float(s[2 * i + 1]), factor, -ref));
+                        l += x + y;
+                        w[i] = bits(__floats2half2_rn(x, y));
+                    }
+                    tmem_st16(ts + c * 16, w);            // over columns of S that have been read
+                }
+                tc_wait_st();
+                tc_fence_before();
+                arrive(&sm.pfull[m]);
+            }
+            // ---- out ----
+            if (ok && wk.n_tile > 0) ok = wait(&sm.sfull[m], wk.n_tile & 1);
+            tc_fence_after();
+            const int qi = m * QT + q_in;
+            const bool mine = r < QT * g && qi < nq;
+            const size_t row = (sq.row + i0 + qi) * p.hq + wk.h * g + r % g;
+            const float inv = !ok ? NAN : l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = 0;
+                if (wk.n_tile > 0) {
+                    tmem_ld32(to + c * 32, o);
+                    tc_wait_ld();
+                }
+                if (mine) {
+                    uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + c * 32);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[8 * i + 2 * e]) * inv,
+                                                                           __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+                            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            if (mine && a.lse) a.lse[row] = !ok ? NAN : l > 0.f ? (ref + log2f(l)) * 0.693147180559945309f : -INFINITY;
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------------ keys and values
+        const int i = threadIdx.x - 256;
+        const int row_bytes = p.krow_bytes, run_bytes = kPage * p.kb / 8, vrun = p.vchan_bytes;
+        const int R = ring_slots(p, a.kpc);
+        constexpr int kVPages = D == 128 ? 2 : 1;         // pages a thread takes of the values
+        uint4 rk[8], rv[kVPages][4];
+        int pg[2];                                        // the tile's pages
+        auto pages = [&](int j) {
+            const int lp = wk.tile_start(j) / kPage;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                pg[e] = (lp + e) * kPage < wk.Lq && (lp + e) * kPage <= wk.p_max ? phys_page(p, wk.b, lp + e) : -1;
+        };
+        auto piece = [](const uint8_t* at, int bytes) {
+            if (bytes >= 16) return __ldg(reinterpret_cast<const uint4*>(at));
+            const uint2 x = __ldg(reinterpret_cast<const uint2*>(at));
+            return make_uint4(x.x, x.y, 0, 0);
+        };
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        auto load_keys = [&]() {
+            if (a.kpc) {
+                const int page = i >> 6, cp = i & 63, n = max(1, run_bytes / 16);
+                const uint8_t* blk = p.k_codes + (size_t(max(page ? pg[1] : pg[0], 0)) * p.hkv + wk.h) * size_t(D) * run_bytes;
+                const int ch = min(16, run_bytes);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool have = e < n && (page ? pg[1] : pg[0]) >= 0 && cp < D / 2;
+                    const uint4 x = have ? piece(blk + e * (D * ch) + (2 * cp) * ch, ch) : none;
+                    const uint4 y = have ? piece(blk + e * (D * ch) + (2 * cp + 1) * ch, ch) : none;
+                    if (e < n) {
+                        rk[e] = x;
+                        if (n == 1) rk[1] = y;
+                        if (n == 2) rk[2 + e] = y;
+                        if (n == 4) rk[4 + e] = y;
+                    }
+                }
+            } else {
+                const int page = i >> 6, slot = i & 63;
+                const uint8_t* blk = p.k_codes + (size_t(max(page ? pg[1] : pg[0], 0)) * p.hkv + wk.h) * size_t(kPage) * row_bytes;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    rk[e] = (page ? pg[1] : pg[0]) >= 0 && e * 16 < row_bytes ? piece(blk + e * (kPage * p.kch) + slot * p.kch, p.kch) : none;
+            }
+        };
+        auto load_values = [&]() {
+#pragma unroll
+            for (int e = 0; e < kVPages; ++e) {
+                const int page = D == 128 ? e : i >> 6, ch = i & (D - 1);
+                const uint8_t* blk = p.v_codes + (size_t(max(page ? pg[1] : pg[0], 0)) * p.hkv + wk.h) * size_t(D) * vrun;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    rv[e][c] = (page ? pg[1] : pg[0]) >= 0 && c * 16 < vrun ? piece(blk + c * (D * p.vch) + ch * p.vch, p.vch) : none;
+            }
+        };
+        bool ok = true;
+        if (wk.n_tile > 0) {
+            pages(0);
+            load_keys();
+            load_values();
+        }
+        for (int j = 0; j < wk.n_tile; ++j) {
+            const int st = j & 1, t0 = wk.tile_start(j);
+            const int page = i >> 6, slot = i & 63, x = t0 + i;
+            const int pg_now[2] = {pg[0], pg[1]};
+            // ---- keys ----
+            if (j >= kStages) ok = ok && wait(&sm.kempty[st], ((j >> 1) + 1) & 1);
+            unsigned char* sk = sm.k[st];
+            if (!ok) {
+                // nothing is written; the four warps stop together below
+            } else if (a.kpc) {
+                const int cp = i & 63;
+                const uint32_t* meta = p.k_meta + (size_t(max(page ? pg_now[1] : pg_now[0], 0)) * p.hkv + wk.h) * size_t(kPage / p.kg) * D;
+                if (cp < D / 2 && (page ? pg_now[1] : pg_now[0]) >= 0) {
+                    const int x0 = t0 + page * kPage;
+                    if (p.kb == 4) put_key_pairs<4, D>(p, rk, meta, cp, page, x0, wk.Lq, vn, sk);
+                    if (p.kb == 8) put_key_pairs<8, D>(p, rk, meta, cp, page, x0, wk.Lq, vn, sk);
+                    if (p.kb == 2) put_key_pairs<2, D>(p, rk, meta, cp, page, x0, wk.Lq, vn, sk);
+                    if (p.kb == 1) put_key_pairs<1, D>(p, rk, meta, cp, page, x0, wk.Lq, vn, sk);
+                }
+            } else if ((page ? pg_now[1] : pg_now[0]) >= 0 && x < wk.Lq) {
+                const uint32_t* meta = p.k_meta + ((size_t(page ? pg_now[1] : pg_now[0]) * p.hkv + wk.h) * kPage + slot) * p.nkg;
+                const int row = slot_of(i, vn);
+                if (p.kb == 4) put_key<4, D>(p, rk, meta, sk, row);
+                if (p.kb == 8) put_key<8, D>(p, rk, meta, sk, row);
+                if (p.kb == 2) put_key<2, D>(p, rk, meta, sk, row);
+                if (p.kb == 1) put_key<1, D>(p, rk, meta, sk, row);
+            }
+            if (ok && t0 + kTile > wk.Lq) {               // ring rows: a few lanes each
+                constexpr int kPer = 32 / (D / 8);
+                for (int s0 = (warp - 8) * 32; s0 < (warp - 8) * 32 + 32; s0 += kPer) {
+                    const int s = s0 + lane / (D / 8), y = t0 + s;
+                    const bool have = y >= wk.Lq && y < wk.L;
+                    if (!__any_sync(0xffffffffu, have)) continue;
+                    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    if (have) load8(p.k_win, true, ((size_t(wk.b) * p.hkv + wk.h) * R + y % R) * D + (lane % (D / 8)) * 8, f);
+                    put_row<D>(f, p.rotate ? p.signs : nullptr, false, have ? sk : nullptr, kKeyPitch, slot_of(s, vn), kn);
+                }
+            }
+            if (i == 0) {
+                int hidden = 0;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (pg_now[e] < 0 && t0 + e * kPage < wk.Lq) hidden |= 1 << e;
+                sm.hidden[j & 3] = hidden;
+            }
+            fence_proxy_async();
+            arrive(&sm.kfull[st]);
+            // ---- metadata of the values, as pairs in the order of the codes ----
+            {   // the last tile's are read; and do all four warps go on?
+                uint32_t all;
+                asm volatile(
+                    "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+                    "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+                    : "=r"(all)
+                    : "r"(uint32_t(ok))
+                    : "memory");
+                ok = all != 0;
+                if (!ok) break;
+            }
+            for (int e = i; e < p.nvg * (kTile / 2); e += 128) {
+                const int q = e % (kTile / 2), gi = e / (kTile / 2);
+                uint32_t m[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int o = code_of(2 * q + u, vn), y = t0 + o, ph = o >> 6 ? pg_now[1] : pg_now[0];
+                    m[u] = ph >= 0 && y < wk.Lq && wk.used(y) ? __ldg(v_meta_row(p, ph, wk.h, o & 63) + gi) : 0u;
+                }
+                sm.vscale[gi][q] = __byte_perm(m[0], m[1], 0x5410);
+                sm.vzero[gi][q] = __byte_perm(m[0], m[1], 0x7632);
+            }
+            if (j + 1 < wk.n_tile) {
+                pages(j + 1);
+                load_keys();
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            // ---- values ----
+            if (j >= kStages) ok = wait(&sm.vempty[st], ((j >> 1) + 1) & 1);
+            unsigned char* sv = sm.v[st];
+#pragma unroll
+            for (int e = 0; e < kVPages; ++e) {
+                if (!ok) break;
+                const int vp = D == 128 ? e : i >> 6, ch = i & (D - 1), gi = ch / p.vg;
+                unsigned char* to = sv + ch * 16;
+                if (p.vb == 2) put_value<2, D>(sm, rv[e], gi, vp, to);
+                if (p.vb == 4) put_value<4, D>(sm, rv[e], gi, vp, to);
+                if (p.vb == 8) put_value<8, D>(sm, rv[e], gi, vp, to);
+                if (p.vb == 1) put_value<1, D>(sm, rv[e], gi, vp, to);
+                const int y0 = t0 + vp * kPage;
+                if (y0 + kPage > wk.Lq) {                 // ring positions in their slots (the page's codes gave zeros there)
+                    for (int o = max(0, wk.Lq - y0); o < kPage && y0 + o < wk.L; ++o) {
+                        if (!wk.used(y0 + o)) continue;
+                        const int s = slot_of(vp * kPage + o, vn);
+                        const float f = __bfloat162float(p.v_win[((size_t(wk.b) * p.hkv + wk.h) * R + (y0 + o) % R) * D + ch]);
+                        *reinterpret_cast<__half*>(to + (s >> 3) * (D * 16) + (s & 7) * 2) = to_half(f);
+                    }
+                }
+            }
+            if (j + 1 < wk.n_tile) load_values();
+            fence_proxy_async();
+            arrive(&sm.vfull[st]);
+        }
+    } else {
+        // ------------------------------------------------ products
+        constexpr uint32_t kS = idesc_f16(kRows, kTile), kO = idesc_f16(kRows, D);
+        auto scores = [&](int m, int j) {
+            const uint64_t qd = smem_desc(smem_u32(sm.q[m]), kRows * 16, 128);
+            const uint64_t kd = smem_desc(smem_u32(sm.k[j & 1]), kKeyPitch, 128);
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+                mma_ss(tmem + m * 128, qd + s * (2 * kRows * 16 >> 4), kd + s * (2 * kKeyPitch >> 4), kS, s > 0);
+            tc_commit_warp(&sm.sfull[m]);
+        };
+        auto values = [&](int m, int j) {
+            const uint64_t vd = smem_desc(smem_u32(sm.v[j & 1]), D * 16, 128);
+#pragma unroll
+            for (int s = 0; s < kTile / 16; ++s)
+                tc_mma_ts_warp(tmem + 256 + m * D, tmem + m * 128 + s * 8, vd + s * (2 * D * 16 >> 4), kO, j > 0 || s > 0);
+        };
+        const int n = wk.n_tile;
+        bool ok = n > 0 && wait(&sm.kfull[0], 0);
+        if (ok) {
+            tc_fence_after();
+            scores(0, 0);
+            if (two) scores(1, 0);
+            tc_commit_warp(&sm.kempty[0]);
+        }
+        for (int j = 0; j < n && ok; ++j) {
+            const bool more = j + 1 < n;
+            ok = wait(&sm.vfull[j & 1], (j >> 1) & 1) && wait(&sm.pfull[0], j & 1);
+            if (!ok) break;
+            tc_fence_after();
+            values(0, j);
+            if (more) {
+                ok = wait(&sm.kfull[(j + 1) & 1], ((j + 1) >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                scores(0, j + 1);
+            } else {
+                tc_commit_warp(&sm.sfull[0]);             // the output of block 0
+            }
+            if (two) {
+                ok = wait(&sm.pfull[1], j & 1);
+                if (!ok) break;
+                tc_fence_after();
+                values(1, j);
+            }
+            tc_commit_warp(&sm.vempty[j & 1]);
+            if (two) {
+                if (more)
+                    scores(1, j + 1);
+                else
+                    tc_commit_warp(&sm.sfull[1]);
+            }
+            if (more) tc_commit_warp(&sm.kempty[(j + 1) & 1]);
+        }
+    }
+    // every product has been waited for by the weights' warps, or the waits have given up
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch_d(const Params& p, const Args& a, unsigned* status, cudaStream_t s) {
+    static bool opted[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    constexpr int kBytes = int(sizeof(Smem<D>)) + 128;
+    if (!opted[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(sink_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+        if (e != cudaSuccess) return e;
+        opted[dev] = true;
+    }
+    const int per = 2 * (kRows / p.g);
+    const dim3 grid((a.max_q + per - 1) / per, p.hkv, p.batch);
+    sink_prefill_kernel<D><<<grid, kThreads, kBytes, s>>>(p, a, status);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prefill(const Params& p, const Args& a, unsigned* status, cudaStream_t s) {
+    return p.d == 128 ? launch_d<128>(p, a, status, s) : launch_d<64>(p, a, status, s);
+}
+
+}  // namespace sink
+}  // namespace kvq

@@ -32,9 +32,17 @@ def present(lay, page_table, b: int, L: int) -> np.ndarray:
     return ok
 
 
-def attention(cache: oracle.Cache, page_table, signs, q, n, lens, sinks: int, span: int, scale: float):
+def attention(cache: oracle.Cache, page_table, signs, q, n, lens, sinks: int, span: int, scale: float, exact_q=True,
+              want_tol=False):
     """q fp64 [sum n][Hq][d]; n queries per sequence, its newest.  Returns out, lse (fp64).  Sequences with
-    n > lens are skipped (nan rows)."""
+    n > lens are skipped (nan rows).  With want_tol also how far out and lse may be off where keys, values and weights
+    are rounded to fp16, each by at most u = 2^-11 of itself (and 2^-25, half a subnormal step), and the query too
+    unless exact_q:
+        |score error| <= D = max over visible t of scale * sum_j |q_j| (|k_tj| (u or 2u) + 2^-25),
+        so every weight is off by a factor within exp(+-2D) and lse by at most D;
+        |out error| <= (exp(2D) - 1) sum_t a_t |v_t - o|  +  (2u + 2^-25) sum_t a_t |v_t|  (weights, values).
+    fp32 sums add 2^-24 per term of the same sums: a factor 1.1 on both covers 400 of them in a row at random signs."""
+    u, tol_o, tol_l = 2.0 ** -11, np.zeros(q.shape), np.zeros(q.shape[:2])
     lay = cache.layout
     g, d = lay.num_q_heads // lay.num_kv_heads, lay.head_dim
     k, v = cache.dequantize(lens, max(1, int(np.max(lens))))
@@ -52,17 +60,31 @@ def attention(cache: oracle.Cache, page_table, signs, q, n, lens, sinks: int, sp
         sees = (x <= t) & ((x < sinks) | (t - x < span)) & present(lay, page_table, b, L)[None, :]
         paged = x[0] < paged_len(lay, L)
         for h in range(lay.num_q_heads):
-            kk, vv = k[b, h // g, :L].astype(np.float64), v[b, h // g, :L].astype(np.float64)
+            some = sees.any(0)[:, None]                     # what no query sees may hold anything
+            kk = np.where(some, k[b, h // g, :L].astype(np.float64), 0.0)
+            vv = np.where(some, v[b, h // g, :L].astype(np.float64), 0.0)
             s = np.where(paged, rot[r0:r0 + m, h] @ kk.T, q[r0:r0 + m, h] @ kk.T) * scale
             s = np.where(sees, s, -np.inf)
             top = s.max(-1, keepdims=True, initial=-np.inf)
             w = np.exp(s - np.where(np.isfinite(top), top, 0.0))
             tot = w.sum(-1, keepdims=True)
-            out[r0:r0 + m, h] = np.where(tot > 0, (w @ np.where(sees.any(0)[:, None], vv, 0.0)) / np.where(tot > 0, tot, 1.0), 0.0)
+            out[r0:r0 + m, h] = np.where(tot > 0, (w @ vv) / np.where(tot > 0, tot, 1.0), 0.0)
             with np.errstate(divide="ignore"):
                 lse[r0:r0 + m, h] = (top + np.log(tot))[:, 0]
+            if want_tol:
+                qq = np.abs(rot[r0:r0 + m, h]) if signs is not None else np.abs(q[r0:r0 + m, h])
+                kr = kk if signs is None else np.where(paged[:, None], kk, (kk * signs) @ hadamard(d))
+                D = abs(scale) * (qq @ np.abs(kr).T * u * (1 if exact_q and signs is None else 2)
+                                  + qq.sum(-1, keepdims=True) * 2.0 ** -25)
+                D = np.where(sees, D, 0.0).max(-1, keepdims=True, initial=0.0)
+                a = np.where(tot > 0, w / np.where(tot > 0, tot, 1.0), 0.0)
+                o = out[r0:r0 + m, h]
+                spread = a @ np.abs(vv) + np.abs(o) if m * L > 20000 else (
+                    a[:, :, None] * np.abs(vv[None] - o[:, None])).sum(1)
+                tol_o[r0:r0 + m, h] = 1.1 * (np.expm1(2 * D) * spread + (2 * u + 2.0 ** -25) * (a @ np.abs(vv)))
+                tol_l[r0:r0 + m, h] = 1.1 * D[:, 0] + 2.0 ** -20 * (1 + np.abs(np.where(tot > 0, lse[r0:r0 + m, h][:, None], 0))[:, 0])
         r0 += m
-    return out, lse
+    return (out, lse, tol_o, tol_l) if want_tol else (out, lse)
 
 
 def rows_back(cache: oracle.Cache, page_table, signs, first, n, lens):
@@ -91,11 +113,12 @@ def queries(w: wl.Workload, rows: int, step: int = 0):
     return raw, f.astype(np.float64)
 
 
-def check_bf16(got, want, what="out"):
-    """|got - want| <= 1e-3 + 1e-3*|want| (the kernels' bound) + half a bf16 step of the value that is rounded,
-    which is at most |want| plus that bound."""
+def check_bf16(got, want, what="out", tol=None):
+    """|got - want| <= tol (default: 1e-3 + 1e-3*|want|, the bound of the kernels that take exact codes) + half a bf16
+    step of the value that is rounded, which is at most |want| plus that bound."""
     got = np.asarray(got, np.float64)
-    lim = (1e-3 + 1e-3 * np.abs(want)) * (1 + HALF_BF16) + HALF_BF16 * np.abs(want)
+    tol = 1e-3 + 1e-3 * np.abs(want) if tol is None else tol
+    lim = tol * (1 + HALF_BF16) + HALF_BF16 * np.abs(want) + 1e-30
     err = np.abs(got - want)
     assert got.shape == want.shape
     if got.size and not np.all(err <= lim):
@@ -103,8 +126,9 @@ def check_bf16(got, want, what="out"):
         raise AssertionError(f"{what}: worst at {i}: got {got[i]!r} want {want[i]!r} (max err {np.nanmax(err):.3e})")
 
 
-def check_lse(got, want):
+def check_lse(got, want, tol=None):
     got = np.asarray(got, np.float64)
     fin = np.isfinite(want)
     assert np.array_equal(np.isfinite(got), fin) and np.all(got[~fin] == want[~fin])
-    np.testing.assert_allclose(got[fin], want[fin], atol=1e-3, rtol=1e-3)
+    tol = 1e-3 + 1e-3 * np.abs(want) if tol is None else tol
+    assert np.all(np.abs(got[fin] - want[fin]) <= tol[fin])
