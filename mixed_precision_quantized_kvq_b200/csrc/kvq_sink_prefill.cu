@@ -18,9 +18,12 @@
 //   0-3, 4-7   weights of block 0 and 1: thread = row.  S from tensor memory
 //              twice (maximum, then weights), P back over S as fp16.  O is
 //              rescaled only when a row's maximum has grown by more than 2^8.
-//   8-11       reconstruct: thread = position for keys, channel for values
-//              (keys with groups along positions: thread = two channels).
-//   12         issues the products.
+//   8-11       reconstruct keys: thread = position (groups along positions: two
+//              channels).  12-15 values: thread = channel.  Codes and metadata
+//              are loaded a tile ahead, page numbers two.
+// The first warp of a block also issues its products (a warp for that alone
+// would cost every thread a quarter of its registers): it has to wait for them
+// anyway.
 // Operands are 8x16-byte core matrices without swizzle, all 16-byte pieces of
 // the same eight columns together, which makes the writers' 16-byte stores
 // contiguous over a warp.  A word holds the codes (i, i + n/2) in the same
@@ -40,7 +43,7 @@ using namespace ptx;
 
 constexpr int kRows = 128;                    // rows of a block
 constexpr int kTile = 128;                    // positions of a tile
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 16 * 32;
 constexpr int kStages = 2;
 constexpr uint64_t kLimitNs = 2000000000ull;  // a wait that takes longer gives up
 constexpr float kRefNone = -1e30f;
@@ -62,8 +65,8 @@ struct Smem {
     unsigned char q[2][kQ];
     unsigned char k[kStages][(kK + 127) / 128 * 128];
     unsigned char v[kStages][kV];
-    uint32_t vscale[8][kTile / 2];                      // value scales and zero points of pairs, by group
-    uint32_t vzero[8][kTile / 2];
+    __half vscale[2][8][kTile];                         // value scales and zero points of two tiles: by group, in the
+    __half vzero[2][8][kTile];                          // order of the unpacked codes
     float factor[2][kRows];
     uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages], sfull[2], pfull[2];
     uint32_t tmem;
@@ -218,17 +221,17 @@ __device__ __forceinline__ void load8(const void* src, bool bf16, size_t at, flo
 
 // ---------------------------------------------------------------- keys
 
-// one position's codes (words in `raw`) with their metadata, to row `row` of the key tile
-template <int BITS, int D>
-__device__ __forceinline__ void put_key(const Params& p, const uint4 (&raw)[8], const uint32_t* meta, unsigned char* to, int row) {
+// one position's codes (words in `raw`) with its D/KG metadata words, to row `row` of the key tile
+template <int BITS, int D, int KG>
+__device__ __forceinline__ void put_key(const uint4 (&raw)[8], const uint32_t (&meta)[8], unsigned char* to, int row) {
     constexpr int N = 32 / BITS, W = D / N;              // codes a word, words a row
-    const int kshift = __ffs(p.kg) - 1;
+    if (KG > D) return;                                  // no such layout
     __half2 out[4];
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         const uint4& q = raw[w / 4];
         const uint32_t word = w % 4 == 0 ? q.x : w % 4 == 1 ? q.y : w % 4 == 2 ? q.z : q.w;
-        const uint32_t m0 = __ldg(meta + (w * N >> kshift)), m1 = N > 16 ? __ldg(meta + ((w * N + N / 2) >> kshift)) : m0;
+        const uint32_t m0 = meta[(w * N / KG) & 7], m1 = meta[((w * N + N / 2) / KG) & 7];
         const __half2 scale = half2_of(__byte_perm(m0, m1, 0x5410)), zero = half2_of(__byte_perm(m0, m1, 0x7632));
         __half2 c[N / 2];
         unpack<BITS>(word, c);
@@ -241,6 +244,13 @@ __device__ __forceinline__ void put_key(const Params& p, const uint4 (&raw)[8], 
                     make_uint4(bits(out[0]), bits(out[1]), bits(out[2]), bits(out[3]));
         }
     }
+}
+template <int BITS, int D>
+__device__ __forceinline__ void put_key_of(int kg, const uint4 (&raw)[8], const uint32_t (&meta)[8], unsigned char* to, int row) {
+    if (kg == 32) put_key<BITS, D, 32>(raw, meta, to, row);
+    if (kg == 64) put_key<BITS, D, 64>(raw, meta, to, row);
+    if (kg == 128) put_key<BITS, D, 128>(raw, meta, to, row);
+    if (kg == 16) put_key<BITS, D, 16>(raw, meta, to, row);
 }
 
 // keys with groups along positions: the codes of channels 2*cp and 2*cp + 1 of one page, to rows of the key tile
@@ -282,10 +292,11 @@ __device__ __forceinline__ void put_key_pairs(const Params& p, const uint4 (&raw
 
 // one channel's run of a page to the value tile: pieces of eight slots, D*16 bytes apart
 template <int BITS, int D>
-__device__ __forceinline__ void put_value(const Smem<D>& sm, const uint4 (&raw)[4], int group, int page, unsigned char* to) {
+__device__ __forceinline__ void put_value(const Smem<D>& sm, int buf, const uint4 (&raw)[4], int group, int page,
+                                          unsigned char* to) {
     constexpr int N = 32 / BITS, W = kPage / N;
-    const uint4* scale = reinterpret_cast<const uint4*>(&sm.vscale[group][page * (kPage / 2)]);
-    const uint4* zero = reinterpret_cast<const uint4*>(&sm.vzero[group][page * (kPage / 2)]);
+    const uint4* scale = reinterpret_cast<const uint4*>(&sm.vscale[buf][group][page * kPage]);
+    const uint4* zero = reinterpret_cast<const uint4*>(&sm.vzero[buf][group][page * kPage]);
     __half2 out[4];
     uint4 s4, z4;
 #pragma unroll
@@ -345,8 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sm.kfull[i], 128);
             mbar_init(&sm.vfull[i], 128);
-            mbar_init(&sm.kempty[i], 1);
-            mbar_init(&sm.vempty[i], 1);
+            mbar_init(&sm.kempty[i], two ? 2 : 1);        // a commit of each block
+            mbar_init(&sm.vempty[i], two ? 2 : 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.sfull[i], 1);
@@ -355,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
         sm.failed = 0;
         mbar_fence_init();
     }
-    if (warp == 12) {
+    if (warp == 15) {
         tmem_alloc(&sm.tmem, 512);
         tmem_relinquish();
     }
@@ -399,8 +410,35 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
             const int q_in = r / g;
             const int t = sq.base + i0 + m * QT + min(q_in, QT - 1);
             const int t_first = sq.base + i0 + m * QT, t_last = min(t_first + QT - 1, wk.p_max);
+            constexpr uint32_t kS = idesc_f16(kRows, kTile), kO = idesc_f16(kRows, D);
+            const bool issuer = (warp & 3) == 0;
+            // S = Q K^T of tile j
+            auto scores = [&](int j) -> bool {
+                if (!wait(&sm.kfull[j & 1], (j >> 1) & 1)) return false;
+                tc_fence_after();
+                const uint64_t qd = smem_desc(smem_u32(sm.q[m]), kRows * 16, 128);
+                const uint64_t kd = smem_desc(smem_u32(sm.k[j & 1]), kKeyPitch, 128);
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s)
+                    mma_ss(tmem + m * 128, qd + s * (2 * kRows * 16 >> 4), kd + s * (2 * kKeyPitch >> 4), kS, s > 0);
+                tc_commit_warp(&sm.sfull[m]);
+                tc_commit_warp(&sm.kempty[j & 1]);
+                return true;
+            };
+            // O += P V of tile j, once the block's four warps have written their rows of P
+            auto values = [&](int j) -> bool {
+                if (!wait(&sm.pfull[m], j & 1) || !wait(&sm.vfull[j & 1], (j >> 1) & 1)) return false;
+                tc_fence_after();
+                const uint64_t vd = smem_desc(smem_u32(sm.v[j & 1]), D * 16, 128);
+#pragma unroll
+                for (int s = 0; s < kTile / 16; ++s)
+                    tc_mma_ts_warp(tmem + 256 + m * D, tmem + m * 128 + s * 8, vd + s * (2 * D * 16 >> 4), kO, j > 0 || s > 0);
+                tc_commit_warp(&sm.vempty[j & 1]);
+                return true;
+            };
             float ref = kRefNone, l = 0.f;
             bool ok = true;
+            if (issuer && wk.n_tile > 0) ok = scores(0);
             for (int j = 0; j < wk.n_tile && ok; ++j) {
                 ok = wait(&sm.sfull[m], j & 1);
                 if (!ok) break;
@@ -467,6 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                 tc_wait_st();
                 tc_fence_before();
                 arrive(&sm.pfull[m]);
+                if (issuer) {
+                    ok = values(j);
+                    if (ok && j + 1 < wk.n_tile) ok = scores(j + 1);
+                    if (ok && j + 1 == wk.n_tile) tc_commit_warp(&sm.sfull[m]);   // the output
+                }
             }
             // ---- out ----
             if (ok && wk.n_tile > 0) ok = wait(&sm.sfull[m], wk.n_tile & 1);
@@ -501,19 +544,16 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
             }
             if (mine && a.lse) a.lse[row] = !ok ? NAN : l > 0.f ? (ref + log2f(l)) * 0.693147180559945309f : -INFINITY;
         }
-    } else if (warp < 12) {
-        // ------------------------------------------------ keys and values
-        const int i = threadIdx.x - 256;
-        const int row_bytes = p.krow_bytes, run_bytes = kPage * p.kb / 8, vrun = p.vchan_bytes;
+    } else {
+        // ------------------------------------------------ keys (warps 8-11), values (12-15)
+        const int i = threadIdx.x & 127;
         const int R = ring_slots(p, a.kpc);
-        constexpr int kVPages = D == 128 ? 2 : 1;         // pages a thread takes of the values
-        uint4 rk[8], rv[kVPages][4];
-        int pg[2];                                        // the tile's pages
-        auto pages = [&](int j) {
-            const int lp = wk.tile_start(j) / kPage;
+        // physical pages of tile j, -1 where absent or past what any row sees
+        auto pages = [&](int j, int (&pg)[2]) {
+            const int lp = j < wk.n_tile ? wk.tile_start(j) / kPage : 0;
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                pg[e] = (lp + e) * kPage < wk.Lq && (lp + e) * kPage <= wk.p_max ? phys_page(p, wk.b, lp + e) : -1;
+                pg[e] = j < wk.n_tile && (lp + e) * kPage < wk.Lq && (lp + e) * kPage <= wk.p_max ? phys_page(p, wk.b, lp + e) : -1;
         };
         auto piece = [](const uint8_t* at, int bytes) {
             if (bytes >= 16) return __ldg(reinterpret_cast<const uint4*>(at));
@@ -521,207 +561,191 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
             return make_uint4(x.x, x.y, 0, 0);
         };
         const uint4 none = make_uint4(0, 0, 0, 0);
-        auto load_keys = [&]() {
-            if (a.kpc) {
-                const int page = i >> 6, cp = i & 63, n = max(1, run_bytes / 16);
-                const uint8_t* blk = p.k_codes + (size_t(max(page ? pg[1] : pg[0], 0)) * p.hkv + wk.h) * size_t(D) * run_bytes;
-                const int ch = min(16, run_bytes);
+        int pg[2], pg_next[2];
+        bool ok = true;
+        pages(0, pg);
+        pages(1, pg_next);
+        if (warp < 12) {
+            const int row_bytes = p.krow_bytes, run_bytes = kPage * p.kb / 8;
+            const int page = i >> 6, slot = i & 63;       // kpc: slot = channel pair
+            uint4 raw[8];
+            uint32_t meta[8];
+            auto load = [&](const int (&g2)[2]) {
+                const int ph = page ? g2[1] : g2[0];
+                if (a.kpc) {
+                    const int n = max(1, run_bytes / 16), ch = min(16, run_bytes);
+                    const uint8_t* blk = p.k_codes + (size_t(max(ph, 0)) * p.hkv + wk.h) * size_t(D) * run_bytes;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const bool have = e < n && (page ? pg[1] : pg[0]) >= 0 && cp < D / 2;
-                    const uint4 x = have ? piece(blk + e * (D * ch) + (2 * cp) * ch, ch) : none;
-                    const uint4 y = have ? piece(blk + e * (D * ch) + (2 * cp + 1) * ch, ch) : none;
-                    if (e < n) {
-                        rk[e] = x;
-                        if (n == 1) rk[1] = y;
-                        if (n == 2) rk[2 + e] = y;
-                        if (n == 4) rk[4 + e] = y;
+                    for (int e = 0; e < 4; ++e) {
+                        const bool have = e < n && ph >= 0 && slot < D / 2;
+                        const uint4 x = have ? piece(blk + e * (D * ch) + (2 * slot) * ch, ch) : none;
+                        const uint4 y = have ? piece(blk + e * (D * ch) + (2 * slot + 1) * ch, ch) : none;
+                        if (e < n) {
+                            raw[e] = x;
+                            if (n == 1) raw[1] = y;
+                            if (n == 2) raw[2 + e] = y;
+                            if (n == 4) raw[4 + e] = y;
+                        }
+                    }
+                } else if (ph >= 0) {
+                    const uint8_t* blk = p.k_codes + (size_t(ph) * p.hkv + wk.h) * size_t(kPage) * row_bytes;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (e * 16 < row_bytes) raw[e] = piece(blk + e * (kPage * p.kch) + slot * p.kch, p.kch);
+                    const uint32_t* m = p.k_meta + ((size_t(ph) * p.hkv + wk.h) * kPage + slot) * p.nkg;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (e < p.nkg) meta[e] = __ldg(m + e);
+                }
+            };
+            load(pg);
+            for (int j = 0; j < wk.n_tile; ++j) {
+                const int st = j & 1, t0 = wk.tile_start(j), x = t0 + i, ph = page ? pg[1] : pg[0];
+                if (j >= kStages) ok = wait(&sm.kempty[st], ((j >> 1) + 1) & 1);
+                if (!ok) break;
+                unsigned char* sk = sm.k[st];
+                if (a.kpc) {
+                    const uint32_t* m = p.k_meta + (size_t(max(ph, 0)) * p.hkv + wk.h) * size_t(kPage / p.kg) * D;
+                    if (slot < D / 2 && ph >= 0) {
+                        const int x0 = t0 + page * kPage;
+                        if (p.kb == 4) put_key_pairs<4, D>(p, raw, m, slot, page, x0, wk.Lq, vn, sk);
+                        if (p.kb == 8) put_key_pairs<8, D>(p, raw, m, slot, page, x0, wk.Lq, vn, sk);
+                        if (p.kb == 2) put_key_pairs<2, D>(p, raw, m, slot, page, x0, wk.Lq, vn, sk);
+                        if (p.kb == 1) put_key_pairs<1, D>(p, raw, m, slot, page, x0, wk.Lq, vn, sk);
+                    }
+                } else if (ph >= 0 && x < wk.Lq) {
+                    const int row = slot_of(i, vn);
+                    if (p.kb == 4) put_key_of<4, D>(p.kg, raw, meta, sk, row);
+                    if (p.kb == 8) put_key_of<8, D>(p.kg, raw, meta, sk, row);
+                    if (p.kb == 2) put_key_of<2, D>(p.kg, raw, meta, sk, row);
+                    if (p.kb == 1) put_key_of<1, D>(p.kg, raw, meta, sk, row);
+                }
+                __syncwarp();
+                if (t0 + kTile > wk.Lq) {                 // ring rows: D/8 lanes each, four loads under way at a time
+                    constexpr int kPer = 32 / (D / 8);
+                    const int oct = lane % (D / 8);
+#pragma unroll 1
+                    for (int s0 = (warp - 8) * 32; s0 < (warp - 8) * 32 + 32; s0 += 4 * kPer) {
+                        if (t0 + s0 + 4 * kPer <= wk.Lq || t0 + s0 >= wk.L) continue;
+                        float f[4][8];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int y = t0 + s0 + u * kPer + lane / (D / 8);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) f[u][e] = 0.f;
+                            if (y >= wk.Lq && y < wk.L)
+                                load8(p.k_win, true, ((size_t(wk.b) * p.hkv + wk.h) * R + y % R) * D + oct * 8, f[u]);
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int s = s0 + u * kPer + lane / (D / 8), y = t0 + s;
+                            put_row<D>(f[u], p.rotate ? p.signs : nullptr, false, y >= wk.Lq && y < wk.L ? sk : nullptr, kKeyPitch,
+                                       slot_of(s, vn), kn);
+                        }
                     }
                 }
-            } else {
-                const int page = i >> 6, slot = i & 63;
-                const uint8_t* blk = p.k_codes + (size_t(max(page ? pg[1] : pg[0], 0)) * p.hkv + wk.h) * size_t(kPage) * row_bytes;
+                if (i == 0) {
+                    int hidden = 0;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (pg[e] < 0 && t0 + e * kPage < wk.Lq) hidden |= 1 << e;
+                    sm.hidden[j & 3] = hidden;
+                }
+                fence_proxy_async();
+                arrive(&sm.kfull[st]);
+                pg[0] = pg_next[0];
+                pg[1] = pg_next[1];
+                load(pg);
+                pages(j + 2, pg_next);
+            }
+        } else {
+            const int vrun = p.vchan_bytes;
+            constexpr int kVPages = D == 128 ? 2 : 1;     // pages a thread takes
+            const int ch = i & (D - 1), gi = ch / p.vg;
+            uint4 raw[kVPages][4];
+            uint32_t meta[8];                             // of position i
+            auto load = [&](const int (&g2)[2], int j) {
+#pragma unroll
+                for (int e = 0; e < kVPages; ++e) {
+                    const int ph = (D == 128 ? e : i >> 6) ? g2[1] : g2[0];
+                    const uint8_t* blk = p.v_codes + (size_t(max(ph, 0)) * p.hkv + wk.h) * size_t(D) * vrun;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        raw[e][c] = ph >= 0 && c * 16 < vrun ? piece(blk + c * (D * p.vch) + ch * p.vch, p.vch) : none;
+                }
+                const int ph = i >> 6 ? g2[1] : g2[0], y = j < wk.n_tile ? wk.tile_start(j) + i : 0;
+                const bool have = ph >= 0 && y < wk.Lq && wk.used(y);
+                const uint32_t* m = p.v_meta + ((size_t(max(ph, 0)) * p.hkv + wk.h) * kPage + (i & 63)) * p.nvg;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    rk[e] = (page ? pg[1] : pg[0]) >= 0 && e * 16 < row_bytes ? piece(blk + e * (kPage * p.kch) + slot * p.kch, p.kch) : none;
-            }
-        };
-        auto load_values = [&]() {
+                    if (e < p.nvg) meta[e] = have ? __ldg(m + e) : 0u;
+            };
+            load(pg, 0);
+            for (int j = 0; j < wk.n_tile; ++j) {
+                const int st = j & 1, t0 = wk.tile_start(j);
+                const int at = slot_of(i, vn);
 #pragma unroll
-            for (int e = 0; e < kVPages; ++e) {
-                const int page = D == 128 ? e : i >> 6, ch = i & (D - 1);
-                const uint8_t* blk = p.v_codes + (size_t(max(page ? pg[1] : pg[0], 0)) * p.hkv + wk.h) * size_t(D) * vrun;
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    rv[e][c] = (page ? pg[1] : pg[0]) >= 0 && c * 16 < vrun ? piece(blk + c * (D * p.vch) + ch * p.vch, p.vch) : none;
-            }
-        };
-        bool ok = true;
-        if (wk.n_tile > 0) {
-            pages(0);
-            load_keys();
-            load_values();
-        }
-        for (int j = 0; j < wk.n_tile; ++j) {
-            const int st = j & 1, t0 = wk.tile_start(j);
-            const int page = i >> 6, slot = i & 63, x = t0 + i;
-            const int pg_now[2] = {pg[0], pg[1]};
-            // ---- keys ----
-            if (j >= kStages) ok = ok && wait(&sm.kempty[st], ((j >> 1) + 1) & 1);
-            unsigned char* sk = sm.k[st];
-            if (!ok) {
-                // nothing is written; the four warps stop together below
-            } else if (a.kpc) {
-                const int cp = i & 63;
-                const uint32_t* meta = p.k_meta + (size_t(max(page ? pg_now[1] : pg_now[0], 0)) * p.hkv + wk.h) * size_t(kPage / p.kg) * D;
-                if (cp < D / 2 && (page ? pg_now[1] : pg_now[0]) >= 0) {
-                    const int x0 = t0 + page * kPage;
-                    if (p.kb == 4) put_key_pairs<4, D>(p, rk, meta, cp, page, x0, wk.Lq, vn, sk);
-                    if (p.kb == 8) put_key_pairs<8, D>(p, rk, meta, cp, page, x0, wk.Lq, vn, sk);
-                    if (p.kb == 2) put_key_pairs<2, D>(p, rk, meta, cp, page, x0, wk.Lq, vn, sk);
-                    if (p.kb == 1) put_key_pairs<1, D>(p, rk, meta, cp, page, x0, wk.Lq, vn, sk);
+                for (int e = 0; e < 8; ++e)
+                    if (e < p.nvg) {
+                        sm.vscale[st][e][at] = __ushort_as_half(uint16_t(meta[e]));
+                        sm.vzero[st][e][at] = __ushort_as_half(uint16_t(meta[e] >> 16));
+                    }
+                if (j >= kStages) ok = wait(&sm.vempty[st], ((j >> 1) + 1) & 1);
+                {   // the metadata is there (the other tile's may still be read); and do all four warps go on?
+                    uint32_t all;
+                    asm volatile(
+                        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+                        "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+                        : "=r"(all)
+                        : "r"(uint32_t(ok))
+                        : "memory");
+                    ok = all != 0;
+                    if (!ok) break;
                 }
-            } else if ((page ? pg_now[1] : pg_now[0]) >= 0 && x < wk.Lq) {
-                const uint32_t* meta = p.k_meta + ((size_t(page ? pg_now[1] : pg_now[0]) * p.hkv + wk.h) * kPage + slot) * p.nkg;
-                const int row = slot_of(i, vn);
-                if (p.kb == 4) put_key<4, D>(p, rk, meta, sk, row);
-                if (p.kb == 8) put_key<8, D>(p, rk, meta, sk, row);
-                if (p.kb == 2) put_key<2, D>(p, rk, meta, sk, row);
-                if (p.kb == 1) put_key<1, D>(p, rk, meta, sk, row);
-            }
-            if (ok && t0 + kTile > wk.Lq) {               // ring rows: a few lanes each
-                constexpr int kPer = 32 / (D / 8);
-                for (int s0 = (warp - 8) * 32; s0 < (warp - 8) * 32 + 32; s0 += kPer) {
-                    const int s = s0 + lane / (D / 8), y = t0 + s;
-                    const bool have = y >= wk.Lq && y < wk.L;
-                    if (!__any_sync(0xffffffffu, have)) continue;
-                    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    if (have) load8(p.k_win, true, ((size_t(wk.b) * p.hkv + wk.h) * R + y % R) * D + (lane % (D / 8)) * 8, f);
-                    put_row<D>(f, p.rotate ? p.signs : nullptr, false, have ? sk : nullptr, kKeyPitch, slot_of(s, vn), kn);
-                }
-            }
-            if (i == 0) {
-                int hidden = 0;
+                unsigned char* to = sm.v[st] + ch * 16;
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (pg_now[e] < 0 && t0 + e * kPage < wk.Lq) hidden |= 1 << e;
-                sm.hidden[j & 3] = hidden;
-            }
-            fence_proxy_async();
-            arrive(&sm.kfull[st]);
-            // ---- metadata of the values, as pairs in the order of the codes ----
-            {   // the last tile's are read; and do all four warps go on?
-                uint32_t all;
-                asm volatile(
-                    "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-                    "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
-                    : "=r"(all)
-                    : "r"(uint32_t(ok))
-                    : "memory");
-                ok = all != 0;
-                if (!ok) break;
-            }
-            for (int e = i; e < p.nvg * (kTile / 2); e += 128) {
-                const int q = e % (kTile / 2), gi = e / (kTile / 2);
-                uint32_t m[2];
+                for (int e = 0; e < kVPages; ++e) {
+                    const int vp = D == 128 ? e : i >> 6;
+                    if (p.vb == 2) put_value<2, D>(sm, st, raw[e], gi, vp, to);
+                    if (p.vb == 4) put_value<4, D>(sm, st, raw[e], gi, vp, to);
+                    if (p.vb == 8) put_value<8, D>(sm, st, raw[e], gi, vp, to);
+                    if (p.vb == 1) put_value<1, D>(sm, st, raw[e], gi, vp, to);
+                    const int y0 = t0 + vp * kPage;
+                    if (y0 + kPage > wk.Lq) {             // ring positions in their slots (the codes gave zeros there)
+                        const __nv_bfloat16* win = p.v_win + (size_t(wk.b) * p.hkv + wk.h) * R * D + ch;
+#pragma unroll 1
+                        for (int o0 = 0; o0 < kPage; o0 += 16) {
+                            if (y0 + o0 + 16 <= wk.Lq || y0 + o0 > wk.p_max) continue;
+                            int slot = (y0 + o0) % R;
+                            __nv_bfloat16 f[16];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int o = code_of(2 * q + u, vn), y = t0 + o, ph = o >> 6 ? pg_now[1] : pg_now[0];
-                    m[u] = ph >= 0 && y < wk.Lq && wk.used(y) ? __ldg(v_meta_row(p, ph, wk.h, o & 63) + gi) : 0u;
-                }
-                sm.vscale[gi][q] = __byte_perm(m[0], m[1], 0x5410);
-                sm.vzero[gi][q] = __byte_perm(m[0], m[1], 0x7632);
-            }
-            if (j + 1 < wk.n_tile) {
-                pages(j + 1);
-                load_keys();
-            }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            // ---- values ----
-            if (j >= kStages) ok = wait(&sm.vempty[st], ((j >> 1) + 1) & 1);
-            unsigned char* sv = sm.v[st];
+                            for (int u = 0; u < 16; ++u) {
+                                const int y = y0 + o0 + u;
+                                f[u] = y >= wk.Lq && wk.used(y) ? win[size_t(slot) * D] : __float2bfloat16_rn(0.f);
+                                slot = slot + 1 == R ? 0 : slot + 1;
+                            }
 #pragma unroll
-            for (int e = 0; e < kVPages; ++e) {
-                if (!ok) break;
-                const int vp = D == 128 ? e : i >> 6, ch = i & (D - 1), gi = ch / p.vg;
-                unsigned char* to = sv + ch * 16;
-                if (p.vb == 2) put_value<2, D>(sm, rv[e], gi, vp, to);
-                if (p.vb == 4) put_value<4, D>(sm, rv[e], gi, vp, to);
-                if (p.vb == 8) put_value<8, D>(sm, rv[e], gi, vp, to);
-                if (p.vb == 1) put_value<1, D>(sm, rv[e], gi, vp, to);
-                const int y0 = t0 + vp * kPage;
-                if (y0 + kPage > wk.Lq) {                 // ring positions in their slots (the page's codes gave zeros there)
-                    for (int o = max(0, wk.Lq - y0); o < kPage && y0 + o < wk.L; ++o) {
-                        if (!wk.used(y0 + o)) continue;
-                        const int s = slot_of(vp * kPage + o, vn);
-                        const float f = __bfloat162float(p.v_win[((size_t(wk.b) * p.hkv + wk.h) * R + (y0 + o) % R) * D + ch]);
-                        *reinterpret_cast<__half*>(to + (s >> 3) * (D * 16) + (s & 7) * 2) = to_half(f);
+                            for (int u = 0; u < 16; ++u) {
+                                const int s = slot_of(vp * kPage + o0 + u, vn);
+                                if (y0 + o0 + u >= wk.Lq)
+                                    *reinterpret_cast<__half*>(to + (s >> 3) * (D * 16) + (s & 7) * 2) = to_half(__bfloat162float(f[u]));
+                            }
+                        }
                     }
                 }
+                fence_proxy_async();
+                arrive(&sm.vfull[st]);
+                pg[0] = pg_next[0];
+                pg[1] = pg_next[1];
+                load(pg, j + 1);
+                pages(j + 2, pg_next);
             }
-            if (j + 1 < wk.n_tile) load_values();
-            fence_proxy_async();
-            arrive(&sm.vfull[st]);
-        }
-    } else {
-        // ------------------------------------------------ products
-        constexpr uint32_t kS = idesc_f16(kRows, kTile), kO = idesc_f16(kRows, D);
-        auto scores = [&](int m, int j) {
-            const uint64_t qd = smem_desc(smem_u32(sm.q[m]), kRows * 16, 128);
-            const uint64_t kd = smem_desc(smem_u32(sm.k[j & 1]), kKeyPitch, 128);
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-                mma_ss(tmem + m * 128, qd + s * (2 * kRows * 16 >> 4), kd + s * (2 * kKeyPitch >> 4), kS, s > 0);
-            tc_commit_warp(&sm.sfull[m]);
-        };
-        auto values = [&](int m, int j) {
-            const uint64_t vd = smem_desc(smem_u32(sm.v[j & 1]), D * 16, 128);
-#pragma unroll
-            for (int s = 0; s < kTile / 16; ++s)
-                tc_mma_ts_warp(tmem + 256 + m * D, tmem + m * 128 + s * 8, vd + s * (2 * D * 16 >> 4), kO, j > 0 || s > 0);
-        };
-        const int n = wk.n_tile;
-        bool ok = n > 0 && wait(&sm.kfull[0], 0);
-        if (ok) {
-            tc_fence_after();
-            scores(0, 0);
-            if (two) scores(1, 0);
-            tc_commit_warp(&sm.kempty[0]);
-        }
-        for (int j = 0; j < n && ok; ++j) {
-            const bool more = j + 1 < n;
-            ok = wait(&sm.vfull[j & 1], (j >> 1) & 1) && wait(&sm.pfull[0], j & 1);
-            if (!ok) break;
-            tc_fence_after();
-            values(0, j);
-            if (more) {
-                ok = wait(&sm.kfull[(j + 1) & 1], ((j + 1) >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                scores(0, j + 1);
-            } else {
-                tc_commit_warp(&sm.sfull[0]);             // the output of block 0
-            }
-            if (two) {
-                ok = wait(&sm.pfull[1], j & 1);
-                if (!ok) break;
-                tc_fence_after();
-                values(1, j);
-            }
-            tc_commit_warp(&sm.vempty[j & 1]);
-            if (two) {
-                if (more)
-                    scores(1, j + 1);
-                else
-                    tc_commit_warp(&sm.sfull[1]);
-            }
-            if (more) tc_commit_warp(&sm.kempty[(j + 1) & 1]);
         }
     }
     // every product has been waited for by the weights' warps, or the waits have given up
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) tmem_dealloc(tmem, 512);
+    if (warp == 15) tmem_dealloc(tmem, 512);
 }
 
 template <int D>
