@@ -16,8 +16,8 @@
 // for both blocks, and while one block's exponentials run the tensor cores
 // work on the other block.  Warps:
 //   0-3, 4-7   weights of block 0 and 1: thread = row.  S from tensor memory
-//              twice (maximum, then weights), P back over S as fp16.  O is
-//              rescaled only when a row's maximum has grown by more than 2^8.
+//              once, P back over S as fp16; reference and O are adjusted only
+//              when a score exceeds the reference by more than 14 binades.
 //   8-11       reconstruct keys: thread = position (groups along positions: two
 //              channels).  12-15 values: thread = channel.  Codes and metadata
 //              are loaded a tile ahead, page numbers two.
@@ -53,9 +53,8 @@ constexpr int kKeyPitch = kTile * 16 + 16;    // bytes between 16-byte columns o
 // positions of the halves of pair p in a run of words of N codes
 template <int N>
 __device__ __forceinline__ constexpr int pair_low(int p) { return p / (N / 2) * N + p % (N / 2); }
-// where code i of a run lies once the words are unpacked, and back
+// where code i of a run lies once the words are unpacked
 __device__ __forceinline__ int slot_of(int i, int n) { return (i & ~(n - 1)) + 2 * (i & (n / 2 - 1)) + ((i & (n / 2)) ? 1 : 0); }
-__device__ __forceinline__ int code_of(int s, int n) { return (s & ~(n - 1)) + ((s & (n - 1)) >> 1) + ((s & 1) ? n / 2 : 0); }
 
 template <int D>
 struct Smem {
@@ -104,6 +103,28 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+// two fp32 numbers in one register pair
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
 __device__ __forceinline__ void arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -114,8 +135,6 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_cast<__half2*>(&w); }
-// fp16 range, so that one element out of it does not turn a row into NaN
-__device__ __forceinline__ __half to_half(float x) { return __float2half_rn(fminf(fmaxf(x, -65504.f), 65504.f)); }
 
 // The 16/BITS pairs of a word as exact fp16 numbers.  With 0x6400 above them the ten low bits of a half-word are the
 // mantissa of 1024 + code * 2^position; one exact operation takes both away.
@@ -136,14 +155,17 @@ __device__ __forceinline__ void unpack(uint32_t w, __half2 (&c)[16 / BITS]) {
 
 // the lowest n bits, for any n
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
-// scores of 32 columns whose positions are not in `seen`: minus infinity
-template <int N>
-__device__ __forceinline__ void hide(uint32_t (&s)[32], uint32_t seen) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const int o = (i & ~(N - 1)) + ((i & (N - 1)) >> 1) + ((i & 1) ? N / 2 : 0);
-        if (!(seen & (1u << o))) s[i] = 0xff800000u;
-    }
+// bits of 32 positions to the slots of their codes, n codes a word (slot_of for all of them)
+__device__ __forceinline__ uint32_t slots_of(uint32_t v, int n) {
+    const auto swap = [&](uint32_t mask, int by) {       // exchange the bits of `mask` with those `by` above
+        const uint32_t t = ((v >> by) ^ v) & mask;
+        v ^= t ^ (t << by);
+    };
+    if (n >= 32) swap(0x0000ff00u, 8);
+    if (n >= 16) swap(0x00f000f0u, 4);
+    if (n >= 8) swap(0x0c0c0c0cu, 2);
+    swap(0x22222222u, 1);
+    return v;
 }
 
 // What a CTA works on.
@@ -198,7 +220,7 @@ __device__ __forceinline__ float put_row(float (&x)[8], const int8_t* signs, boo
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int s = slot_of(oct * 8 + i, n);
-        if (to) *reinterpret_cast<__half*>(to + (s >> 3) * pitch + row * 16 + (s & 7) * 2) = to_half(x[i] * up);
+        if (to) *reinterpret_cast<__half*>(to + (s >> 3) * pitch + row * 16 + (s & 7) * 2) = __float2half_rn(x[i] * up);
     }
     return down;
 }
@@ -225,7 +247,6 @@ __device__ __forceinline__ void load8(const void* src, bool bf16, size_t at, flo
 template <int BITS, int D, int KG>
 __device__ __forceinline__ void put_key(const uint4 (&raw)[8], const uint32_t (&meta)[8], unsigned char* to, int row) {
     constexpr int N = 32 / BITS, W = D / N;              // codes a word, words a row
-    if (KG > D) return;                                  // no such layout
     __half2 out[4];
 #pragma unroll
     for (int w = 0; w < W; ++w) {
@@ -249,8 +270,34 @@ template <int BITS, int D>
 __device__ __forceinline__ void put_key_of(int kg, const uint4 (&raw)[8], const uint32_t (&meta)[8], unsigned char* to, int row) {
     if (kg == 32) put_key<BITS, D, 32>(raw, meta, to, row);
     if (kg == 64) put_key<BITS, D, 64>(raw, meta, to, row);
-    if (kg == 128) put_key<BITS, D, 128>(raw, meta, to, row);
+    if (D >= 128 && kg == 128) put_key<BITS, D, D >= 128 ? 128 : 64>(raw, meta, to, row);
     if (kg == 16) put_key<BITS, D, 16>(raw, meta, to, row);
+}
+
+// a ring row to row `row` of the key tile, in the channel order of words of N codes
+template <int N, int D>
+__device__ __forceinline__ void put_ring_key(const __nv_bfloat16* src, unsigned char* to, int row) {
+    constexpr int C = N > 8 ? N : 8;                     // channels that are exchanged among themselves
+#pragma unroll 2
+    for (int c0 = 0; c0 < D; c0 += C) {
+        uint32_t u[C / 2];
+#pragma unroll
+        for (int i = 0; i < C / 8; ++i) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + c0) + i);
+            u[4 * i] = v.x, u[4 * i + 1] = v.y, u[4 * i + 2] = v.z, u[4 * i + 3] = v.w;
+        }
+        const auto at = [&](int ch) { return __uint_as_float(ch & 1 ? u[ch / 2] & 0xffff0000u : u[ch / 2] << 16); };
+        uint32_t out[C / 2];
+#pragma unroll
+        for (int q = 0; q < C / 2; ++q) {
+            const int low = pair_low<N>(q);
+            out[q] = bits(__floats2half2_rn(at(low), at(low + N / 2)));
+        }
+#pragma unroll
+        for (int i = 0; i < C / 8; ++i)
+            *reinterpret_cast<uint4*>(to + (c0 / 8 + i) * kKeyPitch + row * 16) =
+                make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+    }
 }
 
 // keys with groups along positions: the codes of channels 2*cp and 2*cp + 1 of one page, to rows of the key tile
@@ -322,6 +369,43 @@ __device__ __forceinline__ void put_value(const Smem<D>& sm, int buf, const uint
     }
 }
 
+// one channel of the ring positions of a page (positions y0 ..), in the order of words of N codes
+template <int N, int D>
+__device__ __forceinline__ void put_ring_value(const Work& wk, const __nv_bfloat16* win, int R, int y0, int page, unsigned char* to) {
+    constexpr int C = N > 16 ? N : 16;                   // positions that are loaded at a time
+#pragma unroll 1
+    for (int o0 = 0; o0 < kPage; o0 += C) {
+        if (y0 + o0 + C <= wk.Lq || y0 + o0 > wk.p_max) continue;
+        int slot = (y0 + o0) % R;
+        __half f[C];
+#pragma unroll
+        for (int u = 0; u < C; ++u) {
+            const int y = y0 + o0 + u;
+            f[u] = __float2half_rn(y >= wk.Lq && wk.used(y) ? __bfloat162float(win[size_t(slot) * D]) : 0.f);
+            slot = slot + 1 == R ? 0 : slot + 1;
+        }
+        unsigned char* col = to + (page * kPage + o0) / 8 * (D * 16);
+        if (y0 + o0 >= wk.Lq) {
+#pragma unroll
+            for (int k = 0; k < C / 8; ++k) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int low = pair_low<N>(4 * k + e);
+                    w[e] = bits(__halves2half2(f[low], f[low + N / 2]));
+                }
+                *reinterpret_cast<uint4*>(col + k * (D * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        } else {                                         // the page's last positions are among them
+#pragma unroll
+            for (int u = 0; u < C; ++u) {
+                const int s = slot_of(u, N);
+                if (y0 + o0 + u >= wk.Lq) *reinterpret_cast<__half*>(col + (s >> 3) * (D * 16) + (s & 7) * 2) = f[u];
+            }
+        }
+    }
+}
+
 // ---------------------------------------------------------------- the kernel
 
 template <int D>
@@ -370,20 +454,30 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
         tmem_alloc(&sm.tmem, 512);
         tmem_relinquish();
     }
-    {   // queries, two (or four) rows a warp at a time
+    {   // queries
         constexpr int kPer = 32 / (D / 8);
         const float scale = fabsf(a.scale_log2), sign = a.scale_log2 < 0.f ? -1.f : 1.f;
-        for (int r0 = warp * kPer; r0 < 2 * kRows; r0 += kThreads / 32 * kPer) {
-            const int rr = r0 + lane / (D / 8), m = rr / kRows, r = rr % kRows;
-            const int qi = m * QT + r / g, oct = lane % (D / 8);
-            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (r < QT * g && qi < nq)
-                load8(a.q, a.q_bf16, (sq.row + i0 + qi) * a.q_stride + size_t(wk.h * g + r % g) * D + oct * 8, x);
+#pragma unroll 1
+        for (int r0 = warp * (4 * kPer); r0 < 2 * kRows; r0 += kThreads / 32 * (4 * kPer)) {   // four loads under way
+            const int oct = lane % (D / 8);
+            float x[4][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] *= sign;
-            const float down = put_row<D>(x, p.rotate ? p.signs : nullptr, true, sm.q[m], kRows * 16, r, kn);
-            // (never zero: -inf times it has to stay -inf)
-            if (oct == 0) sm.factor[m][r] = fmaxf(scale * down, 1e-37f);
+            for (int u = 0; u < 4; ++u) {
+                const int rr = r0 + u * kPer + lane / (D / 8), m = rr / kRows, r = rr % kRows, qi = m * QT + r / g;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+                if (r < QT * g && qi < nq)
+                    load8(a.q, a.q_bf16, (sq.row + i0 + qi) * a.q_stride + size_t(wk.h * g + r % g) * D + oct * 8, x[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int rr = r0 + u * kPer + lane / (D / 8), m = rr / kRows, r = rr % kRows;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[u][i] *= sign;
+                const float down = put_row<D>(x[u], p.rotate ? p.signs : nullptr, true, sm.q[m], kRows * 16, r, kn);
+                // (never zero: -inf times it has to stay -inf)
+                if (oct == 0) sm.factor[m][r] = fmaxf(scale * down, 1e-37f);
+            }
         }
     }
     fence_proxy_async();
@@ -454,53 +548,70 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                     if ((hidden >> (c >> 1)) & 1) v &= ~below(wk.Lq - x);
                     return v;
                 };
-                auto mask = [&](int c) {
-                    const uint32_t v = seen(c);
-                    if (vn == 16) hide<16>(s, v);
-                    if (vn == 8) hide<8>(s, v);
-                    if (vn == 4) hide<4>(s, v);
-                    if (vn == 32) hide<32>(s, v);
-                };
-                float mx = -INFINITY;
+                // Weights against the reference of the tiles before.  Should a score lie more than 2^14 above it (the first
+                // tile's always do), the reference is raised, and O and the tile's weights so far are brought down to it.
+                uint64_t l2 = 0;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     tmem_ld32(ts + c * 32, s);
                     tc_wait_ld();
-                    if (!whole) mask(c);
+                    if (!whole) {
+                        const uint32_t v = slots_of(seen(c), vn);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
-                }
-                const float need = mx * factor;
-                if (__any_sync(0xffffffffu, need > ref + 8.f)) {
-                    const float up = fmaxf(ref, need), f = ex2(ref - up);
-                    ref = up;
-                    l *= f;
-                    if (j > 0) {                          // the product with the last tile's values is done: S came after it
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            tmem_ld32(to + c * 32, s);
+                        for (int i = 0; i < 32; ++i)
+                            if (!(v & (1u << i))) s[i] = 0xff800000u;
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        mx[e] = __uint_as_float(s[8 * e]);
+#pragma unroll
+                        for (int i = 1; i < 8; ++i) mx[e] = fmaxf(mx[e], __uint_as_float(s[8 * e + i]));
+                    }
+                    const float need = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * factor;
+                    if (__any_sync(0xffffffffu, need > ref + 14.f)) {
+                        const float up = fmaxf(ref, need), f = ex2(ref - up);
+                        ref = up;
+                        l *= f;
+                        l2 = mul2(l2, pack2(f, f));
+                        const __half2 h = __float2half2_rn(f);
+                        for (int e = 0; e < c; ++e) {
+                            uint32_t w[16];
+                            tmem_ld16(ts + e * 16, w);
                             tc_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * f);
-                            tmem_st32(to + c * 32, s);
+                            for (int i = 0; i < 16; ++i) w[i] = bits(__hmul2(half2_of(w[i]), h));
+                            tmem_st16(ts + e * 16, w);
                         }
-                        tc_wait_st();
+                        if (j > 0)                        // the product with the last tile's values is done: S came after it
+                            for (int e = 0; e < D / 16; ++e) {
+                                uint32_t o[16];
+                                tmem_ld16(to + e * 16, o);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tmem_st16(to + e * 16, o);
+                            }
                     }
-                }
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld32(ts + c * 32, s);
-                    tc_wait_ld();
-                    if (!whole) mask(c);
+                    const uint64_t f2 = pack2(factor, factor), r2 = pack2(-ref, -ref);
                     uint32_t w[16];
+                    uint64_t part[2] = {0, 0};
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float x = ex2(fmaf(__uint_as_float(s[2 * i]), factor, -ref));
-                        const float y = ex2(fmaf(__uint_as_float(s[2 * i + 1]), factor, -ref));
-                        l += x + y;
+                        float x, y;
+                        unpack2(fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), f2, r2), x, y);
+                        x = ex2(x);
+                        y = ex2(y);
+                        part[i & 1] = add2(part[i & 1], pack2(x, y));
                         w[i] = bits(__floats2half2_rn(x, y));
                     }
+                    l2 = add2(l2, add2(part[0], part[1]));
                     tmem_st16(ts + c * 16, w);            // over columns of S that have been read
+                }
+                {
+                    float x, y;
+                    unpack2(l2, x, y);
+                    l += x + y;
                 }
                 tc_wait_st();
                 tc_fence_before();
@@ -548,12 +659,18 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
         // ------------------------------------------------ keys (warps 8-11), values (12-15)
         const int i = threadIdx.x & 127;
         const int R = ring_slots(p, a.kpc);
-        // physical pages of tile j, -1 where absent or past what any row sees
+        // table entries of tile j's pages (-1 past what any row sees); looked at a tile later, so nothing waits for them
         auto pages = [&](int j, int (&pg)[2]) {
             const int lp = j < wk.n_tile ? wk.tile_start(j) / kPage : 0;
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                pg[e] = j < wk.n_tile && (lp + e) * kPage < wk.Lq && (lp + e) * kPage <= wk.p_max ? phys_page(p, wk.b, lp + e) : -1;
+            for (int e = 0; e < 2; ++e) {
+                const bool have = j < wk.n_tile && (lp + e) * kPage < wk.Lq && (lp + e) * kPage <= wk.p_max && lp + e < p.max_pages;
+                pg[e] = have ? __ldg(p.page_table + size_t(wk.b) * p.max_pages + lp + e) : -1;
+            }
+        };
+        auto present = [&](int (&pg)[2]) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) pg[e] = pg[e] < p.num_pages ? max(pg[e], -1) : -1;
         };
         auto piece = [](const uint8_t* at, int bytes) {
             if (bytes >= 16) return __ldg(reinterpret_cast<const uint4*>(at));
@@ -565,6 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
         bool ok = true;
         pages(0, pg);
         pages(1, pg_next);
+        present(pg);
         if (warp < 12) {
             const int row_bytes = p.krow_bytes, run_bytes = kPage * p.kb / 8;
             const int page = i >> 6, slot = i & 63;       // kpc: slot = channel pair
@@ -621,7 +739,17 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                     if (p.kb == 1) put_key_of<1, D>(p.kg, raw, meta, sk, row);
                 }
                 __syncwarp();
-                if (t0 + kTile > wk.Lq) {                 // ring rows: D/8 lanes each, four loads under way at a time
+                if (t0 + kTile > wk.Lq && !p.rotate) {    // ring rows
+                    if (x >= wk.Lq && x < wk.L) {
+                        const __nv_bfloat16* src = p.k_win + ((size_t(wk.b) * p.hkv + wk.h) * R + x % R) * D;
+                        const int row = slot_of(i, vn);
+                        if (kn == 8) put_ring_key<8, D>(src, sk, row);
+                        if (kn == 2) put_ring_key<2, D>(src, sk, row);
+                        if (kn == 4) put_ring_key<4, D>(src, sk, row);
+                        if (kn == 16) put_ring_key<16, D>(src, sk, row);
+                        if (kn == 32) put_ring_key<32, D>(src, sk, row);
+                    }
+                } else if (t0 + kTile > wk.Lq) {          // rotated first: D/8 lanes a row, four loads under way at a time
                     constexpr int kPer = 32 / (D / 8);
                     const int oct = lane % (D / 8);
 #pragma unroll 1
@@ -639,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
                             const int s = s0 + u * kPer + lane / (D / 8), y = t0 + s;
-                            put_row<D>(f[u], p.rotate ? p.signs : nullptr, false, y >= wk.Lq && y < wk.L ? sk : nullptr, kKeyPitch,
+                            put_row<D>(f[u], p.signs, false, y >= wk.Lq && y < wk.L ? sk : nullptr, kKeyPitch,
                                        slot_of(s, vn), kn);
                         }
                     }
@@ -655,6 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                 arrive(&sm.kfull[st]);
                 pg[0] = pg_next[0];
                 pg[1] = pg_next[1];
+                present(pg);
                 load(pg);
                 pages(j + 2, pg_next);
             }
@@ -705,38 +834,24 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                 unsigned char* to = sm.v[st] + ch * 16;
 #pragma unroll
                 for (int e = 0; e < kVPages; ++e) {
-                    const int vp = D == 128 ? e : i >> 6;
+                    const int vp = D == 128 ? e : i >> 6, y0 = t0 + vp * kPage;
                     if (p.vb == 2) put_value<2, D>(sm, st, raw[e], gi, vp, to);
                     if (p.vb == 4) put_value<4, D>(sm, st, raw[e], gi, vp, to);
                     if (p.vb == 8) put_value<8, D>(sm, st, raw[e], gi, vp, to);
                     if (p.vb == 1) put_value<1, D>(sm, st, raw[e], gi, vp, to);
-                    const int y0 = t0 + vp * kPage;
-                    if (y0 + kPage > wk.Lq) {             // ring positions in their slots (the codes gave zeros there)
+                    if (y0 + kPage > wk.Lq) {             // ring positions (the page's codes gave zeros there)
                         const __nv_bfloat16* win = p.v_win + (size_t(wk.b) * p.hkv + wk.h) * R * D + ch;
-#pragma unroll 1
-                        for (int o0 = 0; o0 < kPage; o0 += 16) {
-                            if (y0 + o0 + 16 <= wk.Lq || y0 + o0 > wk.p_max) continue;
-                            int slot = (y0 + o0) % R;
-                            __nv_bfloat16 f[16];
-#pragma unroll
-                            for (int u = 0; u < 16; ++u) {
-                                const int y = y0 + o0 + u;
-                                f[u] = y >= wk.Lq && wk.used(y) ? win[size_t(slot) * D] : __float2bfloat16_rn(0.f);
-                                slot = slot + 1 == R ? 0 : slot + 1;
-                            }
-#pragma unroll
-                            for (int u = 0; u < 16; ++u) {
-                                const int s = slot_of(vp * kPage + o0 + u, vn);
-                                if (y0 + o0 + u >= wk.Lq)
-                                    *reinterpret_cast<__half*>(to + (s >> 3) * (D * 16) + (s & 7) * 2) = to_half(__bfloat162float(f[u]));
-                            }
-                        }
+                        if (p.vb == 2) put_ring_value<16, D>(wk, win, R, y0, vp, to);
+                        if (p.vb == 4) put_ring_value<8, D>(wk, win, R, y0, vp, to);
+                        if (p.vb == 8) put_ring_value<4, D>(wk, win, R, y0, vp, to);
+                        if (p.vb == 1) put_ring_value<32, D>(wk, win, R, y0, vp, to);
                     }
                 }
                 fence_proxy_async();
                 arrive(&sm.vfull[st]);
                 pg[0] = pg_next[0];
                 pg[1] = pg_next[1];
+                present(pg);
                 load(pg, j + 1);
                 pages(j + 2, pg_next);
             }
