@@ -19,7 +19,7 @@
 //              once, P back over S as fp16; reference and O are adjusted only
 //              when a score exceeds the reference by more than 14 binades.
 //   8-11       reconstruct keys: thread = position (groups along positions: two
-//              channels).  12-15 values: thread = channel.  Codes and metadata
+//              channels).  12-19 values: thread = channel of a page.  Codes and metadata
 //              are loaded a tile ahead, page numbers two.
 // The first warp of a block also issues its products (a warp for that alone
 // would cost every thread a quarter of its registers): it has to wait for them
@@ -43,12 +43,13 @@ using namespace ptx;
 
 constexpr int kRows = 128;                    // rows of a block
 constexpr int kTile = 128;                    // positions of a tile
-constexpr int kThreads = 16 * 32;
+constexpr int kThreads = 20 * 32;
+constexpr int kKeyThreads = 128, kValueThreads = 256;
 constexpr int kStages = 2;
 constexpr uint64_t kLimitNs = 2000000000ull;  // a wait that takes longer gives up
 constexpr float kRefNone = -1e30f;
-constexpr int kKeyPitch = kTile * 16 + 16;    // bytes between 16-byte columns of the key tile: the extra piece puts
-                                              // neighbouring columns in different banks (keys by channel pairs)
+constexpr int kKeyPitch = kTile * 16 + 16;    // bytes between 16-byte columns of the key tile and of the queries: the
+constexpr int kQueryPitch = kRows * 16 + 16;  // extra piece puts neighbouring columns of a row in different banks
 
 // positions of the halves of pair p in a run of words of N codes
 template <int N>
@@ -58,10 +59,10 @@ __device__ __forceinline__ int slot_of(int i, int n) { return (i & ~(n - 1)) + 2
 
 template <int D>
 struct Smem {
-    static constexpr int kQ = D / 8 * kRows * 16;       // one block's queries
+    static constexpr int kQ = D / 8 * kQueryPitch;      // one block's queries
     static constexpr int kK = D / 8 * kKeyPitch;
     static constexpr int kV = kTile / 8 * D * 16;
-    unsigned char q[2][kQ];
+    unsigned char q[2][(kQ + 127) / 128 * 128];
     unsigned char k[kStages][(kK + 127) / 128 * 128];
     unsigned char v[kStages][kV];
     __half vscale[2][8][kTile];                         // value scales and zero points of two tiles: by group, in the
@@ -73,14 +74,28 @@ struct Smem {
     int failed;
 };
 
+// One thread issues the products of a tile and their commits (all of them the same thread).
+__device__ __forceinline__ bool elected() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(e)::"memory");
+    return e != 0;
+}
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(0), "r"(0), "r"(0), "r"(0)
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(0)
         : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(0)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 // instruction descriptor: fp16 A and B (K-major), fp32 accumulator
 constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24); }
@@ -241,6 +256,26 @@ __device__ __forceinline__ void load8(const void* src, bool bf16, size_t at, flo
     }
 }
 
+// a row or run of `bytes` (a power of two from 8 to 16 * M) in 16-byte pieces `pitch` bytes apart
+template <int M>
+__device__ __forceinline__ void load_pieces(uint4* to, const uint8_t* at, int pitch, int bytes) {
+    if (bytes == 8) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(at));
+        to[0] = make_uint4(x.x, x.y, 0, 0);
+        return;
+    }
+    to[0] = __ldg(reinterpret_cast<const uint4*>(at));
+    if (M >= 2 && bytes >= 32) to[1] = __ldg(reinterpret_cast<const uint4*>(at + pitch));
+    if (M >= 4 && bytes >= 64) {
+#pragma unroll
+        for (int e = 2; e < 4; ++e) to[e] = __ldg(reinterpret_cast<const uint4*>(at + e * pitch));
+    }
+    if (M >= 8 && bytes >= 128) {
+#pragma unroll
+        for (int e = 4; e < 8; ++e) to[e] = __ldg(reinterpret_cast<const uint4*>(at + e * pitch));
+    }
+}
+
 // ---------------------------------------------------------------- keys
 
 // one position's codes (words in `raw`) with its D/KG metadata words, to row `row` of the key tile
@@ -305,12 +340,11 @@ template <int BITS, int D>
 __device__ __forceinline__ void put_key_pairs(const Params& p, const uint4 (&raw)[8], const uint32_t* meta, int cp, int page,
                                               int x0, int Lq, int vn, unsigned char* to) {
     constexpr int N = 32 / BITS, W = kPage / N;          // codes a word, words a run
-    constexpr int H = (W + 3) / 4;                       // 16-byte pieces a run
     const int kshift = __ffs(p.kg) - 1;
     unsigned char* col = to + (cp >> 2) * kKeyPitch + (cp & 3) * 4;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-        const uint4 &a = raw[w / 4], &b = raw[H + w / 4];
+        const uint4 &a = raw[w / 4], &b = raw[4 + w / 4];
         const uint32_t wa = w % 4 == 0 ? a.x : w % 4 == 1 ? a.y : w % 4 == 2 ? a.z : a.w;
         const uint32_t wb = w % 4 == 0 ? b.x : w % 4 == 1 ? b.y : w % 4 == 2 ? b.z : b.w;
         __half2 ca[N / 2], cb[N / 2];
@@ -413,7 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                                                                    const __grid_constant__ Args a, unsigned* status) {
     extern __shared__ unsigned char raw_smem[];
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw_smem) + 127) & ~uintptr_t(127));
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // (the same in every lane, which the compiler knows after the exchange: operands of the products stay uniform)
+    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) / 32, 0), lane = threadIdx.x % 32;
     Work wk;
     wk.b = blockIdx.z;
     wk.h = blockIdx.y;
@@ -438,8 +473,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
     // ---- set up ----
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sm.kfull[i], 128);
-            mbar_init(&sm.vfull[i], 128);
+            mbar_init(&sm.kfull[i], kKeyThreads);
+            mbar_init(&sm.vfull[i], kValueThreads);
             mbar_init(&sm.kempty[i], two ? 2 : 1);        // a commit of each block
             mbar_init(&sm.vempty[i], two ? 2 : 1);
         }
@@ -474,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                 const int rr = r0 + u * kPer + lane / (D / 8), m = rr / kRows, r = rr % kRows;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[u][i] *= sign;
-                const float down = put_row<D>(x[u], p.rotate ? p.signs : nullptr, true, sm.q[m], kRows * 16, r, kn);
+                const float down = put_row<D>(x[u], p.rotate ? p.signs : nullptr, true, sm.q[m], kQueryPitch, r, kn);
                 // (never zero: -inf times it has to stay -inf)
                 if (oct == 0) sm.factor[m][r] = fmaxf(scale * down, 1e-37f);
             }
@@ -506,28 +541,36 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
             const int t_first = sq.base + i0 + m * QT, t_last = min(t_first + QT - 1, wk.p_max);
             constexpr uint32_t kS = idesc_f16(kRows, kTile), kO = idesc_f16(kRows, D);
             const bool issuer = (warp & 3) == 0;
+            const uint64_t qd = smem_desc(smem_u32(sm.q[m]), kQueryPitch, 128);
+            const uint64_t kd = smem_desc(smem_u32(sm.k[0]), kKeyPitch, 128), vd = smem_desc(smem_u32(sm.v[0]), D * 16, 128);
             // S = Q K^T of tile j
             auto scores = [&](int j) -> bool {
                 if (!wait(&sm.kfull[j & 1], (j >> 1) & 1)) return false;
                 tc_fence_after();
-                const uint64_t qd = smem_desc(smem_u32(sm.q[m]), kRows * 16, 128);
-                const uint64_t kd = smem_desc(smem_u32(sm.k[j & 1]), kKeyPitch, 128);
+                if (elected()) {
+                    const uint64_t k = kd + uint64_t((j & 1) * (int(sizeof(sm.k[0])) >> 4));
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s)
-                    mma_ss(tmem + m * 128, qd + s * (2 * kRows * 16 >> 4), kd + s * (2 * kKeyPitch >> 4), kS, s > 0);
-                tc_commit_warp(&sm.sfull[m]);
-                tc_commit_warp(&sm.kempty[j & 1]);
+                    for (int s = 0; s < D / 16; ++s)
+                        mma_ss(tmem + m * 128, qd + s * (2 * kQueryPitch >> 4), k + s * (2 * kKeyPitch >> 4), kS, s > 0);
+                    commit(&sm.sfull[m]);
+                    commit(&sm.kempty[j & 1]);
+                }
+                __syncwarp();
                 return true;
             };
             // O += P V of tile j, once the block's four warps have written their rows of P
             auto values = [&](int j) -> bool {
                 if (!wait(&sm.pfull[m], j & 1) || !wait(&sm.vfull[j & 1], (j >> 1) & 1)) return false;
                 tc_fence_after();
-                const uint64_t vd = smem_desc(smem_u32(sm.v[j & 1]), D * 16, 128);
+                if (elected()) {
+                    const uint64_t v = vd + uint64_t((j & 1) * (int(sizeof(sm.v[0])) >> 4));
 #pragma unroll
-                for (int s = 0; s < kTile / 16; ++s)
-                    tc_mma_ts_warp(tmem + 256 + m * D, tmem + m * 128 + s * 8, vd + s * (2 * D * 16 >> 4), kO, j > 0 || s > 0);
-                tc_commit_warp(&sm.vempty[j & 1]);
+                    for (int s = 0; s < kTile / 16; ++s)
+                        mma_ts(tmem + 256 + m * D, tmem + m * 128 + s * 8, v + s * (2 * D * 16 >> 4), kO, j > 0 || s > 0);
+                    commit(&sm.vempty[j & 1]);
+                    if (j + 1 == wk.n_tile) commit(&sm.sfull[m]);   // the output
+                }
+                __syncwarp();
                 return true;
             };
             float ref = kRefNone, l = 0.f;
@@ -619,7 +662,6 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                 if (issuer) {
                     ok = values(j);
                     if (ok && j + 1 < wk.n_tile) ok = scores(j + 1);
-                    if (ok && j + 1 == wk.n_tile) tc_commit_warp(&sm.sfull[m]);   // the output
                 }
             }
             // ---- out ----
@@ -656,8 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
             if (mine && a.lse) a.lse[row] = !ok ? NAN : l > 0.f ? (ref + log2f(l)) * 0.693147180559945309f : -INFINITY;
         }
     } else {
-        // ------------------------------------------------ keys (warps 8-11), values (12-15)
-        const int i = threadIdx.x & 127;
+        // ------------------------------------------------ keys (warps 8-11), values (12-19)
         const int R = ring_slots(p, a.kpc);
         // table entries of tile j's pages (-1 past what any row sees); looked at a tile later, so nothing waits for them
         auto pages = [&](int j, int (&pg)[2]) {
@@ -672,18 +713,13 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
 #pragma unroll
             for (int e = 0; e < 2; ++e) pg[e] = pg[e] < p.num_pages ? max(pg[e], -1) : -1;
         };
-        auto piece = [](const uint8_t* at, int bytes) {
-            if (bytes >= 16) return __ldg(reinterpret_cast<const uint4*>(at));
-            const uint2 x = __ldg(reinterpret_cast<const uint2*>(at));
-            return make_uint4(x.x, x.y, 0, 0);
-        };
-        const uint4 none = make_uint4(0, 0, 0, 0);
         int pg[2], pg_next[2];
         bool ok = true;
         pages(0, pg);
         pages(1, pg_next);
         present(pg);
         if (warp < 12) {
+            const int i = threadIdx.x - 256;
             const int row_bytes = p.krow_bytes, run_bytes = kPage * p.kb / 8;
             const int page = i >> 6, slot = i & 63;       // kpc: slot = channel pair
             uint4 raw[8];
@@ -691,25 +727,15 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
             auto load = [&](const int (&g2)[2]) {
                 const int ph = page ? g2[1] : g2[0];
                 if (a.kpc) {
-                    const int n = max(1, run_bytes / 16), ch = min(16, run_bytes);
-                    const uint8_t* blk = p.k_codes + (size_t(max(ph, 0)) * p.hkv + wk.h) * size_t(D) * run_bytes;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const bool have = e < n && ph >= 0 && slot < D / 2;
-                        const uint4 x = have ? piece(blk + e * (D * ch) + (2 * slot) * ch, ch) : none;
-                        const uint4 y = have ? piece(blk + e * (D * ch) + (2 * slot + 1) * ch, ch) : none;
-                        if (e < n) {
-                            raw[e] = x;
-                            if (n == 1) raw[1] = y;
-                            if (n == 2) raw[2 + e] = y;
-                            if (n == 4) raw[4 + e] = y;
-                        }
+                    const int ch = min(16, run_bytes);
+                    const uint8_t* run = p.k_codes + (size_t(max(ph, 0)) * p.hkv + wk.h) * size_t(D) * run_bytes + 2 * slot * ch;
+                    if (ph >= 0 && slot < D / 2) {
+                        load_pieces<4>(raw, run, D * 16, run_bytes);
+                        load_pieces<4>(raw + 4, run + ch, D * 16, run_bytes);
                     }
                 } else if (ph >= 0) {
-                    const uint8_t* blk = p.k_codes + (size_t(ph) * p.hkv + wk.h) * size_t(kPage) * row_bytes;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (e * 16 < row_bytes) raw[e] = piece(blk + e * (kPage * p.kch) + slot * p.kch, p.kch);
+                    load_pieces<8>(raw, p.k_codes + (size_t(ph) * p.hkv + wk.h) * size_t(kPage) * row_bytes + slot * p.kch,
+                                   kPage * 16, row_bytes);
                     const uint32_t* m = p.k_meta + ((size_t(ph) * p.hkv + wk.h) * kPage + slot) * p.nkg;
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -788,57 +814,53 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                 pages(j + 2, pg_next);
             }
         } else {
-            const int vrun = p.vchan_bytes;
-            constexpr int kVPages = D == 128 ? 2 : 1;     // pages a thread takes
-            const int ch = i & (D - 1), gi = ch / p.vg;
-            uint4 raw[kVPages][4];
-            uint32_t meta[8];                             // of position i
+            const int i = threadIdx.x - 384, vrun = p.vchan_bytes;
+            const int ch = i & (D - 1), gi = ch / p.vg, vp = (i / D) & 1;    // page of the tile
+            const bool active = i < 2 * D;
+            const int position = i & 127, g0 = i >> 7;    // metadata: position, groups g0, g0 + 2, ...
+            const int at = slot_of(position, vn);
+            uint4 raw[4];
+            uint32_t meta[4];
             auto load = [&](const int (&g2)[2], int j) {
+                const int ph = vp ? g2[1] : g2[0];
 #pragma unroll
-                for (int e = 0; e < kVPages; ++e) {
-                    const int ph = (D == 128 ? e : i >> 6) ? g2[1] : g2[0];
-                    const uint8_t* blk = p.v_codes + (size_t(max(ph, 0)) * p.hkv + wk.h) * size_t(D) * vrun;
+                for (int c = 0; c < 4; ++c) raw[c] = make_uint4(0, 0, 0, 0);
+                if (ph >= 0 && active)
+                    load_pieces<4>(raw, p.v_codes + (size_t(ph) * p.hkv + wk.h) * size_t(D) * vrun + ch * p.vch, D * 16, vrun);
+                const int pm = position >> 6 ? g2[1] : g2[0], y = j < wk.n_tile ? wk.tile_start(j) + position : 0;
+                const bool have = pm >= 0 && y < wk.Lq && wk.used(y);
+                const uint32_t* m = p.v_meta + ((size_t(max(pm, 0)) * p.hkv + wk.h) * kPage + (position & 63)) * p.nvg;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        raw[e][c] = ph >= 0 && c * 16 < vrun ? piece(blk + c * (D * p.vch) + ch * p.vch, p.vch) : none;
-                }
-                const int ph = i >> 6 ? g2[1] : g2[0], y = j < wk.n_tile ? wk.tile_start(j) + i : 0;
-                const bool have = ph >= 0 && y < wk.Lq && wk.used(y);
-                const uint32_t* m = p.v_meta + ((size_t(max(ph, 0)) * p.hkv + wk.h) * kPage + (i & 63)) * p.nvg;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e < p.nvg) meta[e] = have ? __ldg(m + e) : 0u;
+                for (int e = 0; e < 4; ++e)
+                    if (g0 + 2 * e < p.nvg) meta[e] = have ? __ldg(m + g0 + 2 * e) : 0u;
             };
             load(pg, 0);
             for (int j = 0; j < wk.n_tile; ++j) {
-                const int st = j & 1, t0 = wk.tile_start(j);
-                const int at = slot_of(i, vn);
+                const int st = j & 1, y0 = wk.tile_start(j) + vp * kPage;
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e < p.nvg) {
-                        sm.vscale[st][e][at] = __ushort_as_half(uint16_t(meta[e]));
-                        sm.vzero[st][e][at] = __ushort_as_half(uint16_t(meta[e] >> 16));
+                for (int e = 0; e < 4; ++e)
+                    if (g0 + 2 * e < p.nvg) {
+                        sm.vscale[st][g0 + 2 * e][at] = __ushort_as_half(uint16_t(meta[e]));
+                        sm.vzero[st][g0 + 2 * e][at] = __ushort_as_half(uint16_t(meta[e] >> 16));
                     }
                 if (j >= kStages) ok = wait(&sm.vempty[st], ((j >> 1) + 1) & 1);
-                {   // the metadata is there (the other tile's may still be read); and do all four warps go on?
+                {   // the metadata is there (the other tile's may still be read); and do all the warps go on?
                     uint32_t all;
                     asm volatile(
                         "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-                        "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+                        "barrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
                         : "=r"(all)
-                        : "r"(uint32_t(ok))
+                        : "r"(uint32_t(ok)), "n"(kValueThreads)
                         : "memory");
                     ok = all != 0;
                     if (!ok) break;
                 }
                 unsigned char* to = sm.v[st] + ch * 16;
-#pragma unroll
-                for (int e = 0; e < kVPages; ++e) {
-                    const int vp = D == 128 ? e : i >> 6, y0 = t0 + vp * kPage;
-                    if (p.vb == 2) put_value<2, D>(sm, st, raw[e], gi, vp, to);
-                    if (p.vb == 4) put_value<4, D>(sm, st, raw[e], gi, vp, to);
-                    if (p.vb == 8) put_value<8, D>(sm, st, raw[e], gi, vp, to);
-                    if (p.vb == 1) put_value<1, D>(sm, st, raw[e], gi, vp, to);
+                if (active) {
+                    if (p.vb == 2) put_value<2, D>(sm, st, raw, gi, vp, to);
+                    if (p.vb == 4) put_value<4, D>(sm, st, raw, gi, vp, to);
+                    if (p.vb == 8) put_value<8, D>(sm, st, raw, gi, vp, to);
+                    if (p.vb == 1) put_value<1, D>(sm, st, raw, gi, vp, to);
                     if (y0 + kPage > wk.Lq) {             // ring positions (the page's codes gave zeros there)
                         const __nv_bfloat16* win = p.v_win + (size_t(wk.b) * p.hkv + wk.h) * R * D + ch;
                         if (p.vb == 2) put_ring_value<16, D>(wk, win, R, y0, vp, to);
