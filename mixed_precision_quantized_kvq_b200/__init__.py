@@ -106,7 +106,7 @@ def _ptr(t: Optional[torch.Tensor]):
         return None
     if not t.is_contiguous():
         raise ValueError("tensor must be contiguous")
-    return C.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _check(t: Optional[torch.Tensor], name: str, dtypes, numel: Optional[int] = None,
@@ -337,21 +337,45 @@ def kvq_prefill_attention(layout: Layout, cache: PagedCache, q: torch.Tensor, cu
           _ptr(cu_q), _ptr(lens), int(max_q), C.c_float(sm_scale), _ptr(out), _ptr(lse), _stream(stream))
 
 
-def _check_rows(q: torch.Tensor, name: str, rows: Optional[int], heads: int, d: int) -> Tuple[int, int]:
+# The calls below take a decode step's time themselves, so their checks make
+# one pass over a good argument and leave the message to _check.
+
+def _need(t, name: str, dtypes, numel: int, dev: int, optional: bool = False):
+    """_check, returning the address (None for an absent optional tensor)."""
+    if t is None and optional:
+        return None
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == dev and t.dtype in dtypes
+            and t.is_contiguous() and t.numel() == numel):
+        return t.data_ptr()
+    _check(t, name, dtypes, numel)
+    raise ValueError(f"{name} is not usable")
+
+
+def _need_rows(q, name: str, rows: Optional[int], heads: int, d: int):
     """q is [rows][heads][d] with dense [heads][d] rows that may lie apart
-    (a slice of a wider projection); returns (rows, elements between rows)."""
+    (a slice of a wider projection); returns (address, dtype code, rows,
+    elements between rows, current device)."""
     if not isinstance(q, torch.Tensor):
         raise ValueError(f"{name} must be a torch.Tensor")
-    if q.dim() != 3 or q.shape[1] != heads or q.shape[2] != d or (rows is not None and q.shape[0] != rows):
+    shape = q.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or (rows is not None and shape[0] != rows):
         raise ValueError(f"{name} must have shape [{'rows' if rows is None else rows}][{heads}][{d}], "
-                         f"got {list(q.shape)}")
-    if q.stride(2) != 1 or (heads > 1 and q.stride(1) != d):
-        raise ValueError(f"{name} must have contiguous [{heads}][{d}] rows, got strides {q.stride()}")
-    if q.device.type != "cuda" or q.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} must be a CUDA tensor on the current device, got {q.device}")
+                         f"got {list(shape)}")
+    stride = q.stride()
+    if stride[2] != 1 or (heads > 1 and stride[1] != d):
+        raise ValueError(f"{name} must have contiguous [{heads}][{d}] rows, got strides {stride}")
+    if not q.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor, got {q.device}")
+    dev = torch.cuda.current_device()
+    if q.get_device() != dev:
+        raise ValueError(f"{name} is on {q.device}, not on the current CUDA device cuda:{dev}")
     if q.dtype not in _FLOAT_IN:
         raise ValueError(f"{name} must have dtype torch.bfloat16 or torch.float32, got {q.dtype}")
-    return q.shape[0], q.stride(0) if q.shape[0] > 1 else heads * d
+    return q.data_ptr(), _dtype_code(q), shape[0], stride[0] if shape[0] > 1 else heads * d, dev
+
+
+def _stream_of(stream, dev: int):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def kvq_sink_decode_attention(layout: Layout, cache: PagedCache, q: torch.Tensor, lens: torch.Tensor, max_len: int,
@@ -360,13 +384,13 @@ def kvq_sink_decode_attention(layout: Layout, cache: PagedCache, q: torch.Tensor
     """kvq.h kvq_sink_decode_attention: q [B][Hq][d] (rows may lie apart) -> out bf16 [B][Hq][d], lse fp32 [B][Hq];
     the query of a sequence sees its first `sinks` and its newest `span` cached positions."""
     B, Hq, d = cache.batch, layout.num_q_heads, layout.head_dim
-    _, stride = _check_rows(q, "q", B, Hq, d)
-    _check(lens, "lens", _I32, B)
-    _check(out, "out", _BF16, B * Hq * d)
-    _check(lse, "lse", _F32, B * Hq, optional=True)
-    _call("kvq_sink_decode_attention", C.byref(layout.c()), C.byref(cache.c()), C.c_void_p(q.data_ptr()),
-          _dtype_code(q), stride, _ptr(lens), int(max_len), int(sinks), int(span), C.c_float(sm_scale), _ptr(out),
-          _ptr(lse), _stream(stream))
+    qp, qt, _, stride, dev = _need_rows(q, "q", B, Hq, d)
+    rc = lib().kvq_sink_decode_attention(
+        C.byref(layout.c()), C.byref(cache.c()), qp, qt, stride, _need(lens, "lens", _I32, B, dev), int(max_len),
+        int(sinks), int(span), sm_scale, _need(out, "out", _BF16, B * Hq * d, dev),
+        _need(lse, "lse", _F32, B * Hq, dev, True), _stream_of(stream, dev))
+    if rc != KVQ_OK:
+        raise KVQError("kvq_sink_decode_attention", rc)
 
 
 def kvq_sink_prefill_attention(layout: Layout, cache: PagedCache, q: torch.Tensor, cu_q: torch.Tensor,
@@ -376,14 +400,13 @@ def kvq_sink_prefill_attention(layout: Layout, cache: PagedCache, q: torch.Tenso
     q [total_q][Hq][d], rows may lie apart), causal, over its first `sinks` positions and the newest `span`
     positions up to each query -> out bf16 [total_q][Hq][d], lse fp32 [total_q][Hq]."""
     B, Hq, d = cache.batch, layout.num_q_heads, layout.head_dim
-    T, stride = _check_rows(q, "q", None, Hq, d)
-    _check(cu_q, "cu_q", _I32, B + 1)
-    _check(lens, "lens", _I32, B)
-    _check(out, "out", _BF16, T * Hq * d)
-    _check(lse, "lse", _F32, T * Hq, optional=True)
-    _call("kvq_sink_prefill_attention", C.byref(layout.c()), C.byref(cache.c()), C.c_void_p(q.data_ptr()),
-          _dtype_code(q), stride, _ptr(cu_q), _ptr(lens), int(max_q), int(sinks), int(span), C.c_float(sm_scale),
-          _ptr(out), _ptr(lse), _stream(stream))
+    qp, qt, T, stride, dev = _need_rows(q, "q", None, Hq, d)
+    rc = lib().kvq_sink_prefill_attention(
+        C.byref(layout.c()), C.byref(cache.c()), qp, qt, stride, _need(cu_q, "cu_q", _I32, B + 1, dev),
+        _need(lens, "lens", _I32, B, dev), int(max_q), int(sinks), int(span), sm_scale,
+        _need(out, "out", _BF16, T * Hq * d, dev), _need(lse, "lse", _F32, T * Hq, dev, True), _stream_of(stream, dev))
+    if rc != KVQ_OK:
+        raise KVQError("kvq_sink_prefill_attention", rc)
 
 
 def kvq_read_back(layout: Layout, cache: PagedCache, first: torch.Tensor, cu_rows: torch.Tensor, lens: torch.Tensor,
@@ -393,15 +416,17 @@ def kvq_read_back(layout: Layout, cache: PagedCache, first: torch.Tensor, cu_row
     B, row = cache.batch, layout.num_kv_heads * layout.head_dim
     if k_out.dtype != v_out.dtype:
         raise ValueError("k_out and v_out must share a dtype")
-    _check(k_out, "k_out", _FLOAT_IN)
-    if k_out.numel() % row:
+    n = k_out.numel()
+    dev = torch.cuda.current_device() if k_out.is_cuda else -1
+    if n % row:
         raise ValueError(f"k_out must hold whole rows of {row} elements ([rows][Hkv][d])")
-    _check(v_out, "v_out", _FLOAT_IN, k_out.numel())
-    _check(first, "first", _I32, B)
-    _check(cu_rows, "cu_rows", _I32, B + 1)
-    _check(lens, "lens", _I32, B)
-    _call("kvq_read_back", C.byref(layout.c()), C.byref(cache.c()), _ptr(first), _ptr(cu_rows), _ptr(lens),
-          int(max_rows), _ptr(k_out), _ptr(v_out), _dtype_code(k_out), _stream(stream))
+    kp, vp = _need(k_out, "k_out", _FLOAT_IN, n, dev), _need(v_out, "v_out", _FLOAT_IN, n, dev)
+    rc = lib().kvq_read_back(
+        C.byref(layout.c()), C.byref(cache.c()), _need(first, "first", _I32, B, dev),
+        _need(cu_rows, "cu_rows", _I32, B + 1, dev), _need(lens, "lens", _I32, B, dev), int(max_rows), kp, vp,
+        _dtype_code(k_out), _stream_of(stream, dev))
+    if rc != KVQ_OK:
+        raise KVQError("kvq_read_back", rc)
 
 
 def kvq_dequantize(layout: Layout, cache: PagedCache, lens: torch.Tensor, max_len: int,
