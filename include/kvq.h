@@ -411,7 +411,7 @@ int kvq_sink_prefill_attention(const kvq_layout* layout, const kvq_cache* cache,
  * max_rows  host bound on the rows of a sequence (launch size); a sequence
  *           with more rows is skipped and its rows left untouched
  * k_out, v_out 16-byte aligned.  Returns KVQ_ERR_UNSUPPORTED for batch
- * above 65535 or (max_rows/64 + 2) * 2 * num_kv_heads above 2^31 - 1. */
+ * above 65535 or max_rows above 65533 * 64 (4194112). */
 int kvq_read_back(const kvq_layout* layout, const kvq_cache* cache, const int32_t* first,
                   const int32_t* cu_rows, const int32_t* lens, int max_rows, void* k_out,
                   void* v_out, int out_dtype, kvq_stream_t stream);

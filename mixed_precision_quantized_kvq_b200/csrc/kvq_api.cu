@@ -356,8 +356,8 @@ int kvq_read_back(const kvq_layout* layout, const kvq_cache* cache, const int32_
     if (rc) return rc;
     if ((rc = check_cache(layout, cache))) return rc;
     if (out_dtype != KVQ_F32 && out_dtype != KVQ_BF16) return KVQ_ERR_INVALID_ARG;
-    if (!first || !cu_rows || !lens || max_rows < 0 || max_rows > INT32_MAX - 128) return KVQ_ERR_INVALID_ARG;
-    if (cache->batch > 65535 || (int64_t(max_rows) / kvq::kPage + 2) * 2 * layout->num_kv_heads > INT32_MAX)
+    if (!first || !cu_rows || !lens || max_rows < 0) return KVQ_ERR_INVALID_ARG;
+    if (cache->batch > 65535 || max_rows > 65533 * kvq::kPage || layout->num_kv_heads > INT32_MAX / 2)
         return KVQ_ERR_UNSUPPORTED;
     if (cache->batch == 0 || max_rows == 0) return KVQ_OK;
     if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return KVQ_ERR_INVALID_ARG;

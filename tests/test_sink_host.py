@@ -46,7 +46,7 @@ def test_prefill_refuses(kw):
     assert prefill(**kw) == BAD
 
 
-@pytest.mark.parametrize("kw", [dict(first=None), dict(cu=None), dict(lens=None), dict(max_rows=-1), dict(max_rows=2 ** 31 - 1),
+@pytest.mark.parametrize("kw", [dict(first=None), dict(cu=None), dict(lens=None), dict(max_rows=-1),
                                 dict(k=None), dict(v=None), dict(k=P + 8), dict(v=P + 4), dict(dt=3)])
 def test_read_back_refuses(kw):
     assert back(**kw) == BAD
@@ -65,6 +65,11 @@ def test_layouts_and_caches_are_checked(call):
     assert call(cache=(c, keep)) == UNSUP
     c, keep = _fake_cache(batch=0)
     assert call(cache=(c, keep)) == OK
+
+
+def test_read_back_bound_on_rows():
+    assert back(max_rows=2 ** 31 - 1) == UNSUP
+    assert back(max_rows=65533 * 64 + 1) == UNSUP
 
 
 def test_nothing_to_do():
