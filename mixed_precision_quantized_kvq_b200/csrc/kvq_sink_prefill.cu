@@ -5,25 +5,28 @@
 //
 //     S = Q K^T,  P = 2^(factor S - ref) where visible,  O += P V,  l += P 1
 //
-// over tiles of 128 positions (two pages), with a running reference exponent
-// per query row; O / l is rounded to bf16.  Bound by the tensor cores and the
+// over tiles of 64 positions (a page), with a running reference exponent per
+// query row; O / l is rounded to bf16.  Bound by the tensor cores and the
 // exponentials (one per visible pair: 16 a clock and SM, which takes as long as
-// the two products at head_dim 128).
+// the two products at head_dim 128), in practice by the issue slots that the
+// exponentials and the reconstruction share.
 //
 // One CTA per SM takes 256 rows of one (sequence, kv-head): two blocks of 128,
 // each 128/g queries with their g heads.  Reconstructing a key or value costs
 // about two issue slots an element, so a tile is reconstructed once, to fp16,
-// for both blocks, and while one block's exponentials run the tensor cores
-// work on the other block.  Warps:
+// for both blocks.  Tensor memory holds two score tiles and the output of each
+// block: the next tile's scores are there before a tile's weights are done, so
+// the weights never wait for a product.  Warps:
 //   0-3, 4-7   weights of block 0 and 1: thread = row.  S from tensor memory
 //              once, P back over S as fp16; reference and O are adjusted only
 //              when a score exceeds the reference by more than 14 binades.
-//   8-11       reconstruct keys: thread = position (groups along positions: two
-//              channels).  12-19 values: thread = channel of a page.  Codes and metadata
-//              are loaded a tile ahead, page numbers two.
-// The first warp of a block also issues its products (a warp for that alone
-// would cost every thread a quarter of its registers): it has to wait for them
-// anyway.
+//   8-11       reconstruct keys: thread = half the channels of a position
+//              (groups along positions: two channels of half the positions).
+//   12-19      values: thread = half the positions of a channel.  Codes and
+//              metadata are loaded a tile ahead, page numbers two.
+//   20         issues the products (21-23 fill its warp group).
+// The kernel is launched with 80 registers a thread, 1920 over its 24 warps; the
+// roles then take 96, 112, 64 and 48: 8*96 + 4*112 + 8*64 + 4*48 = 1920.
 // Operands are 8x16-byte core matrices without swizzle, all 16-byte pieces of
 // the same eight columns together, which makes the writers' 16-byte stores
 // contiguous over a warp.  A word holds the codes (i, i + n/2) in the same
@@ -42,10 +45,10 @@ namespace {
 using namespace ptx;
 
 constexpr int kRows = 128;                    // rows of a block
-constexpr int kTile = 128;                    // positions of a tile
-constexpr int kThreads = 20 * 32;
+constexpr int kTile = kPage;                  // positions of a tile
+constexpr int kThreads = 24 * 32;
 constexpr int kKeyThreads = 128, kValueThreads = 256;
-constexpr int kStages = 2;
+constexpr int kStages = 4;
 constexpr uint64_t kLimitNs = 2000000000ull;  // a wait that takes longer gives up
 constexpr float kRefNone = -1e30f;
 constexpr int kKeyPitch = kTile * 16 + 16;    // bytes between 16-byte columns of the key tile and of the queries: the
@@ -65,12 +68,14 @@ struct Smem {
     unsigned char q[2][(kQ + 127) / 128 * 128];
     unsigned char k[kStages][(kK + 127) / 128 * 128];
     unsigned char v[kStages][kV];
-    __half vscale[2][8][kTile];                         // value scales and zero points of two tiles: by group, in the
-    __half vzero[2][8][kTile];                          // order of the unpacked codes
+    alignas(16) __half vscale[2][8][kTile];             // value scales and zero points of two tiles: by group, in the
+    alignas(16) __half vzero[2][8][kTile];              // order of the unpacked codes
     float factor[2][kRows];
-    uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages], sfull[2], pfull[2];
+    uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
+    uint64_t sfull[2][2], pfull[2][2];                  // block, tile % 2
+    uint64_t odone[2], olast[2];                        // a tile's values, the last tile's
     uint32_t tmem;
-    int hidden[4];                                      // tile j % 4: bit i set when page i is absent
+    int hidden[8];                                      // tile % 8: its page is absent
     int failed;
 };
 
@@ -134,10 +139,18 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
     return v;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t v;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-    return v;
+// a load's registers are there once this has run; they pass through it so that nothing that reads them moves before it
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                      "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(r[30]), "+r"(r[31]) : : "memory");
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t v;
@@ -260,65 +273,103 @@ __device__ __forceinline__ void load8(const void* src, bool bf16, size_t at, flo
     }
 }
 
-// a row or run of `bytes` (a power of two from 8 to 16 * M) in 16-byte pieces `pitch` bytes apart
+// where byte `from` of a row or run lies: `chunk` bytes together (16, or 8 for shorter rows and runs), `pitch` apart
+__device__ __forceinline__ int part_offset(int from, int chunk, int pitch) { return from / chunk * pitch + from % chunk; }
+// `bytes` (a power of two from 4 to 16 * M) of a row or run
 template <int M>
-__device__ __forceinline__ void load_pieces(uint4* to, const uint8_t* at, int pitch, int bytes) {
-    if (bytes == 8) {
+__device__ __forceinline__ void load_part(uint4 (&to)[M], const uint8_t* at, int pitch, int bytes) {
+    if (bytes >= 16) {
+        to[0] = __ldg(reinterpret_cast<const uint4*>(at));
+        if (M >= 2 && bytes >= 32) to[M >= 2 ? 1 : 0] = __ldg(reinterpret_cast<const uint4*>(at + pitch));
+        if (M >= 4 && bytes >= 64) {
+            to[M >= 4 ? 2 : 0] = __ldg(reinterpret_cast<const uint4*>(at + 2 * pitch));
+            to[M >= 4 ? 3 : 0] = __ldg(reinterpret_cast<const uint4*>(at + 3 * pitch));
+        }
+    } else if (bytes == 8) {
         const uint2 x = __ldg(reinterpret_cast<const uint2*>(at));
-        to[0] = make_uint4(x.x, x.y, 0, 0);
-        return;
-    }
-    to[0] = __ldg(reinterpret_cast<const uint4*>(at));
-    if (M >= 2 && bytes >= 32) to[1] = __ldg(reinterpret_cast<const uint4*>(at + pitch));
-    if (M >= 4 && bytes >= 64) {
-#pragma unroll
-        for (int e = 2; e < 4; ++e) to[e] = __ldg(reinterpret_cast<const uint4*>(at + e * pitch));
-    }
-    if (M >= 8 && bytes >= 128) {
-#pragma unroll
-        for (int e = 4; e < 8; ++e) to[e] = __ldg(reinterpret_cast<const uint4*>(at + e * pitch));
+        to[0].x = x.x;
+        to[0].y = x.y;
+    } else {
+        to[0].x = __ldg(reinterpret_cast<const uint32_t*>(at));
     }
 }
 
 // ---------------------------------------------------------------- keys
 
-// one position's codes (words in `raw`) with its D/KG metadata words, to row `row` of the key tile
+__device__ __forceinline__ uint32_t word_of(const uint4& q, int w) { return w == 0 ? q.x : w == 1 ? q.y : w == 2 ? q.z : q.w; }
+
+// half the channels (first C0) of a position, codes in `raw`, metadata of their groups, to row `row` of the key tile
 template <int BITS, int D, int KG>
-__device__ __forceinline__ void put_key(const uint4 (&raw)[8], const uint32_t (&meta)[8], unsigned char* to, int row) {
-    constexpr int N = 32 / BITS, W = D / N;              // codes a word, words a row
+__device__ __forceinline__ void put_key(const uint4 (&raw)[4], const uint32_t (&meta)[4], unsigned char* to) {
+    constexpr int N = 32 / BITS, W = D / 2 / N;          // codes a word, words
     __half2 out[4];
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-        const uint4& q = raw[w / 4];
-        const uint32_t word = w % 4 == 0 ? q.x : w % 4 == 1 ? q.y : w % 4 == 2 ? q.z : q.w;
-        const uint32_t m0 = meta[(w * N / KG) & 7], m1 = meta[((w * N + N / 2) / KG) & 7];
+        // groups of the word's low and high codes
+        const uint32_t m0 = meta[w * N / KG % 4], m1 = meta[(w * N + N / 2) / KG % 4];
         const __half2 scale = half2_of(__byte_perm(m0, m1, 0x5410)), zero = half2_of(__byte_perm(m0, m1, 0x7632));
         __half2 c[N / 2];
-        unpack<BITS>(word, c);
+        unpack<BITS>(word_of(raw[w / 4], w % 4), c);
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-            const int s = w * (N / 2) + i;               // pair of the row
+            const int s = w * (N / 2) + i;               // pair
             out[s & 3] = __hfma2(c[i], scale, zero);
             if ((s & 3) == 3)
-                *reinterpret_cast<uint4*>(to + (s >> 2) * kKeyPitch + row * 16) =
-                    make_uint4(bits(out[0]), bits(out[1]), bits(out[2]), bits(out[3]));
+                *reinterpret_cast<uint4*>(to + (s >> 2) * kKeyPitch) = make_uint4(bits(out[0]), bits(out[1]), bits(out[2]), bits(out[3]));
         }
     }
 }
 template <int BITS, int D>
-__device__ __forceinline__ void put_key_of(int kg, const uint4 (&raw)[8], const uint32_t (&meta)[8], unsigned char* to, int row) {
-    if (kg == 32) put_key<BITS, D, 32>(raw, meta, to, row);
-    if (kg == 64) put_key<BITS, D, 64>(raw, meta, to, row);
-    if (D >= 128 && kg == 128) put_key<BITS, D, D >= 128 ? 128 : 64>(raw, meta, to, row);
-    if (kg == 16) put_key<BITS, D, 16>(raw, meta, to, row);
+__device__ __forceinline__ void put_key_of(int kg, const uint4 (&raw)[4], const uint32_t (&meta)[4], unsigned char* to) {
+    if (kg == 16)
+        put_key<BITS, D, 16>(raw, meta, to);
+    else if (kg == 32 || D == 64)
+        put_key<BITS, D, 32>(raw, meta, to);             // (D = 64: half a row is one group of 32 or part of one of 64)
+    else
+        put_key<BITS, D, 64>(raw, meta, to);             // half a row is one group of 64 or half of one of 128
 }
 
-// a ring row to row `row` of the key tile, in the channel order of words of N codes
+// Keys with groups along positions: codes of channels 2*cp (raw[0..1]) and 2*cp + 1 (raw[2..3]) at half the positions of a
+// page, 32 from t0 on, to rows of the key tile.
+template <int BITS, int D>
+__device__ __forceinline__ void put_key_pairs(const uint4 (&raw)[4], const uint32_t* meta, int kshift, int t0, int valid, int vn,
+                                              unsigned char* to) {
+    constexpr int N = 32 / BITS, W = 32 / N;             // codes a word, words a channel
+    int step[5];                                         // the slot of a position is the sum over its bits
+#pragma unroll
+    for (int b = 0; b < 5; ++b) step[b] = slot_of(1 << b, vn) * 16;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        __half2 ca[N / 2], cb[N / 2];
+        unpack<BITS>(word_of(raw[w / 4], w % 4), ca);
+        unpack<BITS>(word_of(raw[2 + w / 4], w % 4), cb);
+        __half2 scale[2], zero[2];                       // of the words' low and high codes' groups
+#pragma unroll
+        for (int h = 0; h < (N > 16 ? 2 : 1); ++h) {
+            const uint2 m = __ldg(reinterpret_cast<const uint2*>(meta + size_t((t0 + w * N + h * (N / 2)) >> kshift) * D));
+            scale[h] = half2_of(__byte_perm(m.x, m.y, 0x5410));
+            zero[h] = half2_of(__byte_perm(m.x, m.y, 0x7632));
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int h = i >= N / 2, t = w * N + i;
+            const __half2 c = half2_of(__byte_perm(bits(ca[i % (N / 2)]), bits(cb[i % (N / 2)]), h ? 0x7632 : 0x5410));
+            const __half2 k = __hfma2(c, scale[N > 16 ? h : 0], zero[N > 16 ? h : 0]);
+            int off = 0;
+#pragma unroll
+            for (int b = 0; b < 5; ++b)
+                if (t & (1 << b)) off += step[b];
+            if (t0 + t < valid) *reinterpret_cast<uint32_t*>(to + off) = bits(k);
+        }
+    }
+}
+
+// half a ring row to its row of the key tile, in the channel order of words of N codes
 template <int N, int D>
-__device__ __forceinline__ void put_ring_key(const __nv_bfloat16* src, unsigned char* to, int row) {
+__device__ __forceinline__ void put_ring_key(const __nv_bfloat16* src, unsigned char* to) {
     constexpr int C = N > 8 ? N : 8;                     // channels that are exchanged among themselves
 #pragma unroll 2
-    for (int c0 = 0; c0 < D; c0 += C) {
+    for (int c0 = 0; c0 < D / 2; c0 += C) {
         uint32_t u[C / 2];
 #pragma unroll
         for (int i = 0; i < C / 8; ++i) {
@@ -334,85 +385,48 @@ __device__ __forceinline__ void put_ring_key(const __nv_bfloat16* src, unsigned 
         }
 #pragma unroll
         for (int i = 0; i < C / 8; ++i)
-            *reinterpret_cast<uint4*>(to + (c0 / 8 + i) * kKeyPitch + row * 16) =
+            *reinterpret_cast<uint4*>(to + (c0 / 8 + i) * kKeyPitch) =
                 make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
-    }
-}
-
-// keys with groups along positions: the codes of channels 2*cp and 2*cp + 1 of one page, to rows of the key tile
-template <int BITS, int D>
-__device__ __forceinline__ void put_key_pairs(const Params& p, const uint4 (&raw)[8], const uint32_t* meta, int cp, int page,
-                                              int x0, int Lq, int vn, unsigned char* to) {
-    constexpr int N = 32 / BITS, W = kPage / N;          // codes a word, words a run
-    const int kshift = __ffs(p.kg) - 1;
-    unsigned char* col = to + (cp >> 2) * kKeyPitch + (cp & 3) * 4;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-        const uint4 &a = raw[w / 4], &b = raw[4 + w / 4];
-        const uint32_t wa = w % 4 == 0 ? a.x : w % 4 == 1 ? a.y : w % 4 == 2 ? a.z : a.w;
-        const uint32_t wb = w % 4 == 0 ? b.x : w % 4 == 1 ? b.y : w % 4 == 2 ? b.z : b.w;
-        __half2 ca[N / 2], cb[N / 2];
-        unpack<BITS>(wa, ca);
-        unpack<BITS>(wb, cb);
-        __half2 scale[2], zero[2];                       // of the words' low and high codes' groups
-#pragma unroll
-        for (int e = 0; e < (N > 16 ? 2 : 1); ++e) {
-            const uint2 m = __ldg(reinterpret_cast<const uint2*>(meta + size_t((w * N + e * (N / 2)) >> kshift) * D + 2 * cp));
-            scale[e] = half2_of(__byte_perm(m.x, m.y, 0x5410));
-            zero[e] = half2_of(__byte_perm(m.x, m.y, 0x7632));
-        }
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int t = w * N + i + e * (N / 2);
-                const __half2 c = half2_of(__byte_perm(bits(ca[i]), bits(cb[i]), e ? 0x7632 : 0x5410));
-                const __half2 k = __hfma2(c, scale[N > 16 ? e : 0], zero[N > 16 ? e : 0]);
-                if (x0 + t < Lq) *reinterpret_cast<uint32_t*>(col + slot_of(page * kPage + t, vn) * 16) = bits(k);
-            }
     }
 }
 
 // ---------------------------------------------------------------- values
 
-// one channel's run of a page to the value tile: pieces of eight slots, D*16 bytes apart
+// half a channel's run of a page to the value tile: pieces of eight slots, D*16 bytes apart
 template <int BITS, int D>
-__device__ __forceinline__ void put_value(const Smem<D>& sm, int buf, const uint4 (&raw)[4], int group, int page,
-                                          unsigned char* to) {
-    constexpr int N = 32 / BITS, W = kPage / N;
-    const uint4* scale = reinterpret_cast<const uint4*>(&sm.vscale[buf][group][page * kPage]);
-    const uint4* zero = reinterpret_cast<const uint4*>(&sm.vzero[buf][group][page * kPage]);
-    __half2 out[4];
-    uint4 s4, z4;
+__device__ __forceinline__ void put_value(const __half* scale, const __half* zero, const uint4 (&raw)[2], unsigned char* to) {
+    constexpr int N = 32 / BITS, W = 32 / N;
+    const uint4 *sp = reinterpret_cast<const uint4*>(scale), *zp = reinterpret_cast<const uint4*>(zero);
+    uint4 s4, z4, out;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-        const uint4& q = raw[w / 4];
-        const uint32_t word = w % 4 == 0 ? q.x : w % 4 == 1 ? q.y : w % 4 == 2 ? q.z : q.w;
         __half2 c[N / 2];
-        unpack<BITS>(word, c);
+        unpack<BITS>(word_of(raw[w / 4], w % 4), c);
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-            const int s = w * (N / 2) + i;               // pair of the run
+            const int s = w * (N / 2) + i;               // pair
             if ((s & 3) == 0) {
-                s4 = scale[s >> 2];
-                z4 = zero[s >> 2];
+                s4 = sp[s >> 2];
+                z4 = zp[s >> 2];
             }
-            const uint32_t sc = (s & 3) == 0 ? s4.x : (s & 3) == 1 ? s4.y : (s & 3) == 2 ? s4.z : s4.w;
-            const uint32_t ze = (s & 3) == 0 ? z4.x : (s & 3) == 1 ? z4.y : (s & 3) == 2 ? z4.z : z4.w;
-            out[s & 3] = __hfma2(c[i], half2_of(sc), half2_of(ze));
-            if ((s & 3) == 3)
-                *reinterpret_cast<uint4*>(to + ((s >> 2) + page * (kPage / 8)) * (D * 16)) =
-                    make_uint4(bits(out[0]), bits(out[1]), bits(out[2]), bits(out[3]));
+            const uint32_t v = bits(__hfma2(c[i], half2_of(word_of(s4, s & 3)), half2_of(word_of(z4, s & 3))));
+            if ((s & 3) == 0) out.x = v;
+            if ((s & 3) == 1) out.y = v;
+            if ((s & 3) == 2) out.z = v;
+            if ((s & 3) == 3) {
+                out.w = v;
+                *reinterpret_cast<uint4*>(to + (s >> 2) * (D * 16)) = out;
+            }
         }
     }
 }
 
-// one channel of the ring positions of a page (positions y0 ..), in the order of words of N codes
+// one channel of the ring positions among 32 positions from y0 on, in the order of words of N codes
 template <int N, int D>
-__device__ __forceinline__ void put_ring_value(const Work& wk, const __nv_bfloat16* win, int R, int y0, int page, unsigned char* to) {
+__device__ __forceinline__ void put_ring_value(const Work& wk, const __nv_bfloat16* win, int R, int y0, unsigned char* to) {
     constexpr int C = N > 16 ? N : 16;                   // positions that are loaded at a time
 #pragma unroll 1
-    for (int o0 = 0; o0 < kPage; o0 += C) {
+    for (int o0 = 0; o0 < 32; o0 += C) {
         if (y0 + o0 + C <= wk.Lq || y0 + o0 > wk.p_max) continue;
         int slot = (y0 + o0) % R;
         __half f[C];
@@ -422,7 +436,7 @@ __device__ __forceinline__ void put_ring_value(const Work& wk, const __nv_bfloat
             f[u] = __float2half_rn(y >= wk.Lq && wk.used(y) ? __bfloat162float(win[size_t(slot) * D]) : 0.f);
             slot = slot + 1 == R ? 0 : slot + 1;
         }
-        unsigned char* col = to + (page * kPage + o0) / 8 * (D * 16);
+        unsigned char* col = to + o0 / 8 * (D * 16);
         if (y0 + o0 >= wk.Lq) {
 #pragma unroll
             for (int k = 0; k < C / 8; ++k) {
@@ -479,17 +493,21 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sm.kfull[i], kKeyThreads);
             mbar_init(&sm.vfull[i], kValueThreads);
-            mbar_init(&sm.kempty[i], two ? 2 : 1);        // a commit of each block
-            mbar_init(&sm.vempty[i], two ? 2 : 1);
+            mbar_init(&sm.kempty[i], 1);
+            mbar_init(&sm.vempty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.sfull[i], 1);
-            mbar_init(&sm.pfull[i], 128);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&sm.sfull[i >> 1][i & 1], 1);
+            mbar_init(&sm.pfull[i >> 1][i & 1], kRows);
         }
+        mbar_init(&sm.odone[0], 1);
+        mbar_init(&sm.odone[1], 1);
+        mbar_init(&sm.olast[0], 1);
+        mbar_init(&sm.olast[1], 1);
         sm.failed = 0;
         mbar_fence_init();
     }
-    if (warp == 15) {
+    if (warp == 20) {
         tmem_alloc(&sm.tmem, 512);
         tmem_relinquish();
     }
@@ -523,158 +541,121 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sm.tmem;                        // S0 S1 O0 O1, 128 (D) columns each
+    const uint32_t tmem = sm.tmem;                        // S of block 0 (two of 64 columns) and 1, O of block 0 (D columns) and 1
 
-    // a wait that gives up is remembered: every role stops at its next one.  The answer is the warp's.
+    // A wait that gives up is remembered: every role stops at its next one that is not over at once.  The answer is the
+    // warp's.
+    auto late = [&](uint32_t bar, int parity) -> bool {
+        const uint64_t begin = globaltimer();
+        for (;;) {
+            if (mbar_try_wait(bar, uint32_t(parity))) return true;
+            if (*reinterpret_cast<volatile int*>(&sm.failed)) return false;
+            if (globaltimer() - begin > kLimitNs) {
+                if (atomicExch(&sm.failed, 1) == 0) atomicAdd(status, 1u);
+                return false;
+            }
+        }
+    };
     auto wait = [&](uint64_t* bar, int parity) -> bool {
-        bool done = !*reinterpret_cast<volatile int*>(&sm.failed) && mbar_wait(bar, uint32_t(parity), kLimitNs);
-        done = __all_sync(0xffffffffu, done);
-        if (!done && lane == 0 && atomicExch(&sm.failed, 1) == 0) atomicAdd(status, 1u);
-        return done;
+        const uint32_t at = smem_u32(bar);
+        bool done = mbar_try_wait(at, uint32_t(parity));
+        if (!done) done = late(at, parity);
+        return __all_sync(0xffffffffu, done);
     };
 
     if (warp < 8) {
         // ------------------------------------------------ weights
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
         const int m = warp >> 2, r = threadIdx.x & 127;
         if (m == 0 || two) {
             const uint32_t lanes = uint32_t(warp & 3) * 32u << 16;
-            const uint32_t ts = tmem + m * 128 + lanes, to = tmem + 256 + m * D + lanes;
+            const uint32_t to = tmem + 256 + m * D + lanes;
             const float factor = sm.factor[m][r];
             const int q_in = r / g;
             const int t = sq.base + i0 + m * QT + min(q_in, QT - 1);
             const int t_first = sq.base + i0 + m * QT, t_last = min(t_first + QT - 1, wk.p_max);
-            constexpr uint32_t kS = idesc_f16(kRows, kTile), kO = idesc_f16(kRows, D);
-            const bool issuer = (warp & 3) == 0;
-            const uint64_t qd = smem_desc(smem_u32(sm.q[m]), kQueryPitch, 128);
-            const uint64_t kd = smem_desc(smem_u32(sm.k[0]), kKeyPitch, 128), vd = smem_desc(smem_u32(sm.v[0]), D * 16, 128);
-            // S = Q K^T of tile j
-            auto scores = [&](int j) -> bool {
-                if (!wait(&sm.kfull[j & 1], (j >> 1) & 1)) return false;
-                tc_fence_after();
-                if (elected()) {
-                    const uint64_t k = kd + uint64_t((j & 1) * (int(sizeof(sm.k[0])) >> 4));
-                    mma_ss<false>(tmem + m * 128, qd, k, kS);
-#pragma unroll
-                    for (int s = 1; s < D / 16; ++s)
-                        mma_ss<true>(tmem + m * 128, qd + s * (2 * kQueryPitch >> 4), k + s * (2 * kKeyPitch >> 4), kS);
-                    commit(&sm.sfull[m]);
-                    commit(&sm.kempty[j & 1]);
-                }
-                __syncwarp();
-                return true;
-            };
-            // O += P V of tile j, once the block's four warps have written their rows of P
-            auto values = [&](int j) -> bool {
-                if (!wait(&sm.pfull[m], j & 1) || !wait(&sm.vfull[j & 1], (j >> 1) & 1)) return false;
-                tc_fence_after();
-                if (elected()) {
-                    const uint64_t v = vd + uint64_t((j & 1) * (int(sizeof(sm.v[0])) >> 4));
-                    if (j == 0)
-                        mma_ts<false>(tmem + 256 + m * D, tmem + m * 128, v, kO);
-                    else
-                        mma_ts<true>(tmem + 256 + m * D, tmem + m * 128, v, kO);
-#pragma unroll
-                    for (int s = 1; s < kTile / 16; ++s)
-                        mma_ts<true>(tmem + 256 + m * D, tmem + m * 128 + s * 8, v + s * (2 * D * 16 >> 4), kO);
-                    commit(&sm.vempty[j & 1]);
-                    if (j + 1 == wk.n_tile) commit(&sm.sfull[m]);   // the output
-                }
-                __syncwarp();
-                return true;
-            };
             float ref = kRefNone, l = 0.f;
             bool ok = true;
-            if (issuer && wk.n_tile > 0) ok = scores(0);
             for (int j = 0; j < wk.n_tile && ok; ++j) {
-                ok = wait(&sm.sfull[m], j & 1);
+                ok = wait(&sm.sfull[m][j & 1], (j >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                const int t0 = wk.tile_start(j), hidden = *reinterpret_cast<volatile int*>(&sm.hidden[j & 3]);
+                const uint32_t ts = tmem + (m * 2 + (j & 1)) * kTile + lanes;
+                uint32_t s[2][32];
+                tmem_ld32(ts, s[0]);
+                tmem_ld32(ts + 32, s[1]);
+                const int t0 = wk.tile_start(j), hidden = *reinterpret_cast<volatile int*>(&sm.hidden[j & 7]);
                 // every row of the block sees the whole tile?
                 const bool whole = !hidden && t0 + kTile - 1 <= t_first && (t_last - t0 < a.span || t0 + kTile <= a.sinks);
-                uint32_t s[32];
-                // bit o: position t0 + 32*c + o is visible to this row
-                auto seen = [&](int c) -> uint32_t {
-                    const int x = t0 + 32 * c;
-                    uint32_t v = below(t - x + 1) & (~below(max(t - a.span, -1) - x + 1) | below(a.sinks - x));
-                    if ((hidden >> (c >> 1)) & 1) v &= ~below(wk.Lq - x);
-                    return v;
-                };
-                // Weights against the reference of the tiles before.  Should a score lie more than 2^14 above it (the first
-                // tile's always do), the reference is raised, and O and the tile's weights so far are brought down to it.
-                uint64_t l2 = 0;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld32(ts + c * 32, s);
-                    tc_wait_ld();
-                    if (!whole) {
-                        const uint32_t v = slots_of(seen(c), vn);
+                tmem_loaded(s[0]);
+                tmem_loaded(s[1]);
+                if (!whole) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        // bit o: position x + o is visible to this row
+                        const int x = t0 + 32 * c;
+                        uint32_t v = below(t - x + 1) & (~below(max(t - a.span, -1) - x + 1) | below(a.sinks - x));
+                        if (hidden) v &= ~below(wk.Lq - x);
+                        v = slots_of(v, vn);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (!(v & (1u << i))) s[i] = 0xff800000u;
+                            if (!(v & (1u << i))) s[c][i] = 0xff800000u;
                     }
-                    float mx[4];
+                }
+                float mx[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        mx[e] = __uint_as_float(s[8 * e]);
+                for (int e = 0; e < 8; ++e) {
+                    mx[e] = __uint_as_float(s[e >> 2][(e & 3) * 8]);
 #pragma unroll
-                        for (int i = 1; i < 8; ++i) mx[e] = fmaxf(mx[e], __uint_as_float(s[8 * e + i]));
-                    }
-                    const float need = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * factor;
-                    if (__any_sync(0xffffffffu, need > ref + 14.f)) {
-                        const float up = fmaxf(ref, need), f = ex2(ref - up);
-                        ref = up;
-                        l *= f;
-                        l2 = mul2(l2, pack2(f, f));
-                        const __half2 h = __float2half2_rn(f);
-                        for (int e = 0; e < c; ++e) {
-                            uint32_t w[16];
-                            tmem_ld16(ts + e * 16, w);
+                    for (int i = 1; i < 8; ++i) mx[e] = fmaxf(mx[e], __uint_as_float(s[e >> 2][(e & 3) * 8 + i]));
+                }
+                const float need = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * factor;
+                // Weights are taken against the reference of the tiles before.  Should a score lie more than 2^14 above it (the
+                // first tile's always do), the reference is raised and O brought down to it.
+                if (__builtin_expect(__any_sync(0xffffffffu, need > ref + 14.f), 0)) {
+                    const float up = fmaxf(ref, need), f = ex2(ref - up);
+                    ref = up;
+                    l *= f;
+                    if (j > 0) {
+                        // (S(j) came after the values of tile j - 2, so the barrier is in phase j - 1 or just past it)
+                        ok = wait(&sm.odone[m], (j - 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int e = 0; e < D / 16; ++e) {
+                            uint32_t o[16];
+                            tmem_ld16(to + e * 16, o);
                             tc_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) w[i] = bits(__hmul2(half2_of(w[i]), h));
-                            tmem_st16(ts + e * 16, w);
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st16(to + e * 16, o);
                         }
-                        if (j > 0)                        // the product with the last tile's values is done: S came after it
-                            for (int e = 0; e < D / 16; ++e) {
-                                uint32_t o[16];
-                                tmem_ld16(to + e * 16, o);
-                                tc_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                tmem_st16(to + e * 16, o);
-                            }
                     }
-                    const uint64_t f2 = pack2(factor, factor), r2 = pack2(-ref, -ref);
-                    uint32_t w[16];
-                    uint64_t part[2] = {0, 0};
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float x, y;
-                        unpack2(fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), f2, r2), x, y);
-                        x = ex2(x);
-                        y = ex2(y);
-                        part[i & 1] = add2(part[i & 1], pack2(x, y));
-                        w[i] = bits(__floats2half2_rn(x, y));
-                    }
-                    l2 = add2(l2, add2(part[0], part[1]));
-                    tmem_st16(ts + c * 16, w);            // over columns of S that have been read
                 }
+                const uint64_t f2 = pack2(factor, factor), r2 = pack2(-ref, -ref);
+                uint64_t part[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    uint32_t* q = &s[i >> 4][2 * (i & 15)];
+                    float x, y;
+                    unpack2(fma2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), f2, r2), x, y);
+                    x = ex2(x);
+                    y = ex2(y);
+                    part[i & 3] = add2(part[i & 3], pack2(x, y));
+                    s[0][i] = bits(__floats2half2_rn(x, y));   // (slot i has been read)
+                }
+                tmem_st32(ts, s[0]);                      // over S
                 {
                     float x, y;
-                    unpack2(l2, x, y);
+                    unpack2(add2(add2(part[0], part[1]), add2(part[2], part[3])), x, y);
                     l += x + y;
                 }
                 tc_wait_st();
                 tc_fence_before();
-                arrive(&sm.pfull[m]);
-                if (issuer) {
-                    ok = values(j);
-                    if (ok && j + 1 < wk.n_tile) ok = scores(j + 1);
-                }
+                arrive(&sm.pfull[m][j & 1]);
             }
             // ---- out ----
-            if (ok && wk.n_tile > 0) ok = wait(&sm.sfull[m], wk.n_tile & 1);
+            if (ok && wk.n_tile > 0) ok = wait(&sm.olast[m], 0);
             tc_fence_after();
             const int qi = m * QT + q_in;
             const bool mine = r < QT * g && qi < nq;
@@ -706,93 +687,95 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
             }
             if (mine && a.lse) a.lse[row] = !ok ? NAN : l > 0.f ? (ref + log2f(l)) * 0.693147180559945309f : -INFINITY;
         }
-    } else {
+    } else if (warp < 20) {
         // ------------------------------------------------ keys (warps 8-11), values (12-19)
         const int R = ring_slots(p, a.kpc);
-        // table entries of tile j's pages (-1 past what any row sees); looked at a tile later, so nothing waits for them
-        auto pages = [&](int j, int (&pg)[2]) {
-            const int lp = j < wk.n_tile ? wk.tile_start(j) / kPage : 0;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const bool have = j < wk.n_tile && (lp + e) * kPage < wk.Lq && (lp + e) * kPage <= wk.p_max && lp + e < p.max_pages;
-                pg[e] = have ? __ldg(p.page_table + size_t(wk.b) * p.max_pages + lp + e) : -1;
-            }
+        // table entry of tile j's page (-1 past what any row sees); looked at a tile later, so nothing waits for it
+        auto page_of = [&](int j) -> int {
+            if (j >= wk.n_tile) return -1;
+            const int lp = wk.tile_start(j) / kPage;
+            return lp * kPage < wk.Lq && lp < p.max_pages ? __ldg(p.page_table + size_t(wk.b) * p.max_pages + lp) : -1;
         };
-        auto present = [&](int (&pg)[2]) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) pg[e] = pg[e] < p.num_pages ? max(pg[e], -1) : -1;
-        };
-        int pg[2], pg_next[2];
+        auto present = [&](int pg) -> int { return pg < p.num_pages ? max(pg, -1) : -1; };
         bool ok = true;
-        pages(0, pg);
-        pages(1, pg_next);
-        present(pg);
+        int pg = present(page_of(0)), pg_next = page_of(1);
         if (warp < 12) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
             const int i = threadIdx.x - 256;
-            const int row_bytes = p.krow_bytes, run_bytes = kPage * p.kb / 8;
-            const int page = i >> 6, slot = i & 63;       // kpc: slot = channel pair
-            uint4 raw[8];
-            uint32_t meta[8];
-            auto load = [&](const int (&g2)[2]) {
-                const int ph = page ? g2[1] : g2[0];
+            const int half = i >> 6, slot = i & 63;       // kpc: half of the positions, channel pair
+            const int run_bytes = kPage * p.kb / 8, ch = min(16, run_bytes), kshift = __ffs(p.kg) - 1;
+            uint4 raw[4];
+            uint32_t meta[4];
+            // this thread's codes and metadata in page 0, and what lies between pages
+            const int part = a.kpc ? run_bytes / 2 : p.krow_bytes / 2, groups = min(4, max(1, D / 2 >> kshift));
+            const size_t code_step = size_t(p.hkv) * kPage * p.krow_bytes, meta_step = size_t(p.hkv) * kPage * p.nkg;
+            const uint8_t* codes = p.k_codes + size_t(wk.h) * kPage * p.krow_bytes +
+                                   (a.kpc ? 2 * slot * ch + part_offset(half * part, ch, D * 16)
+                                          : slot * p.kch + part_offset(half * part, p.kch, kPage * 16));
+            // (tokens: groups from that of channel half * D/2 on: D/2 / kg of them, or the one that holds them all)
+            const uint32_t* metas = p.k_meta + (size_t(wk.h) * kPage + slot) * p.nkg + (half * (D / 2) >> kshift);
+            auto load = [&]() {
+                if (pg < 0) return;
+                const uint8_t* at = codes + pg * code_step;
                 if (a.kpc) {
-                    const int ch = min(16, run_bytes);
-                    const uint8_t* run = p.k_codes + (size_t(max(ph, 0)) * p.hkv + wk.h) * size_t(D) * run_bytes + 2 * slot * ch;
-                    if (ph >= 0 && slot < D / 2) {
-                        load_pieces<4>(raw, run, D * 16, run_bytes);
-                        load_pieces<4>(raw + 4, run + ch, D * 16, run_bytes);
+                    if (slot >= D / 2) return;
+                    uint4 x[2], y[2];
+                    load_part<2>(x, at, D * 16, part);
+                    load_part<2>(y, at + ch, D * 16, part);
+                    raw[0] = x[0], raw[1] = x[1], raw[2] = y[0], raw[3] = y[1];
+                } else {
+                    load_part<4>(raw, at, kPage * 16, part);
+                    const uint32_t* m = metas + pg * meta_step;
+                    meta[0] = __ldg(m);
+                    if (groups >= 2) meta[1] = __ldg(m + 1);
+                    if (groups >= 4) {
+                        meta[2] = __ldg(m + 2);
+                        meta[3] = __ldg(m + 3);
                     }
-                } else if (ph >= 0) {
-                    load_pieces<8>(raw, p.k_codes + (size_t(ph) * p.hkv + wk.h) * size_t(kPage) * row_bytes + slot * p.kch,
-                                   kPage * 16, row_bytes);
-                    const uint32_t* m = p.k_meta + ((size_t(ph) * p.hkv + wk.h) * kPage + slot) * p.nkg;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (e < p.nkg) meta[e] = __ldg(m + e);
                 }
             };
-            load(pg);
+            load();
+#pragma unroll 1
             for (int j = 0; j < wk.n_tile; ++j) {
-                const int st = j & 1, t0 = wk.tile_start(j), x = t0 + i, ph = page ? pg[1] : pg[0];
-                if (j >= kStages) ok = wait(&sm.kempty[st], ((j >> 1) + 1) & 1);
+                const int st = j % kStages, t0 = wk.tile_start(j), x = t0 + slot;
+                if (j >= kStages) ok = wait(&sm.kempty[st], (j / kStages + 1) & 1);
                 if (!ok) break;
                 unsigned char* sk = sm.k[st];
+                unsigned char* row = sk + slot_of(slot, vn) * 16 + half * (D / 16) * kKeyPitch;
                 if (a.kpc) {
-                    const uint32_t* m = p.k_meta + (size_t(max(ph, 0)) * p.hkv + wk.h) * size_t(kPage / p.kg) * D;
-                    if (slot < D / 2 && ph >= 0) {
-                        const int x0 = t0 + page * kPage;
-                        if (p.kb == 4) put_key_pairs<4, D>(p, raw, m, slot, page, x0, wk.Lq, vn, sk);
-                        if (p.kb == 8) put_key_pairs<8, D>(p, raw, m, slot, page, x0, wk.Lq, vn, sk);
-                        if (p.kb == 2) put_key_pairs<2, D>(p, raw, m, slot, page, x0, wk.Lq, vn, sk);
-                        if (p.kb == 1) put_key_pairs<1, D>(p, raw, m, slot, page, x0, wk.Lq, vn, sk);
+                    if (slot < D / 2 && pg >= 0) {
+                        const uint32_t* m = p.k_meta + (size_t(pg) * p.hkv + wk.h) * size_t(kPage >> kshift) * D + 2 * slot;
+                        unsigned char* col = sk + (slot >> 2) * kKeyPitch + (slot & 3) * 4 + half * (32 * 16);
+                        if (p.kb == 4) put_key_pairs<4, D>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
+                        if (p.kb == 8) put_key_pairs<8, D>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
+                        if (p.kb == 2) put_key_pairs<2, D>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
+                        if (p.kb == 1) put_key_pairs<1, D>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
                     }
-                } else if (ph >= 0 && x < wk.Lq) {
-                    const int row = slot_of(i, vn);
-                    if (p.kb == 4) put_key_of<4, D>(p.kg, raw, meta, sk, row);
-                    if (p.kb == 8) put_key_of<8, D>(p.kg, raw, meta, sk, row);
-                    if (p.kb == 2) put_key_of<2, D>(p.kg, raw, meta, sk, row);
-                    if (p.kb == 1) put_key_of<1, D>(p.kg, raw, meta, sk, row);
+                } else if (pg >= 0 && x < wk.Lq) {
+                    if (p.kb == 4) put_key_of<4, D>(p.kg, raw, meta, row);
+                    if (p.kb == 8) put_key_of<8, D>(p.kg, raw, meta, row);
+                    if (p.kb == 2) put_key_of<2, D>(p.kg, raw, meta, row);
+                    if (p.kb == 1) put_key_of<1, D>(p.kg, raw, meta, row);
                 }
                 __syncwarp();
                 if (t0 + kTile > wk.Lq && !p.rotate) {    // ring rows
                     if (x >= wk.Lq && x < wk.L) {
-                        const __nv_bfloat16* src = p.k_win + ((size_t(wk.b) * p.hkv + wk.h) * R + x % R) * D;
-                        const int row = slot_of(i, vn);
-                        if (kn == 8) put_ring_key<8, D>(src, sk, row);
-                        if (kn == 2) put_ring_key<2, D>(src, sk, row);
-                        if (kn == 4) put_ring_key<4, D>(src, sk, row);
-                        if (kn == 16) put_ring_key<16, D>(src, sk, row);
-                        if (kn == 32) put_ring_key<32, D>(src, sk, row);
+                        const __nv_bfloat16* src = p.k_win + ((size_t(wk.b) * p.hkv + wk.h) * R + x % R) * D + half * (D / 2);
+                        if (kn == 8) put_ring_key<8, D>(src, row);
+                        if (kn == 2) put_ring_key<2, D>(src, row);
+                        if (kn == 4) put_ring_key<4, D>(src, row);
+                        if (kn == 16) put_ring_key<16, D>(src, row);
+                        if (kn == 32) put_ring_key<32, D>(src, row);
                     }
-                } else if (t0 + kTile > wk.Lq) {          // rotated first: D/8 lanes a row, four loads under way at a time
+                } else if (t0 + kTile > wk.Lq) {          // rotated first: D/8 lanes a row, two loads under way at a time
                     constexpr int kPer = 32 / (D / 8);
                     const int oct = lane % (D / 8);
 #pragma unroll 1
-                    for (int s0 = (warp - 8) * 32; s0 < (warp - 8) * 32 + 32; s0 += 4 * kPer) {
-                        if (t0 + s0 + 4 * kPer <= wk.Lq || t0 + s0 >= wk.L) continue;
-                        float f[4][8];
+                    for (int s0 = (warp - 8) * 16; s0 < (warp - 8) * 16 + 16; s0 += 2 * kPer) {
+                        if (t0 + s0 + 2 * kPer <= wk.Lq || t0 + s0 >= wk.L) continue;
+                        float f[2][8];
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
+                        for (int u = 0; u < 2; ++u) {
                             const int y = t0 + s0 + u * kPer + lane / (D / 8);
 #pragma unroll
                             for (int e = 0; e < 8; ++e) f[u][e] = 0.f;
@@ -800,59 +783,54 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                                 load8(p.k_win, true, ((size_t(wk.b) * p.hkv + wk.h) * R + y % R) * D + oct * 8, f[u]);
                         }
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
+                        for (int u = 0; u < 2; ++u) {
                             const int s = s0 + u * kPer + lane / (D / 8), y = t0 + s;
-                            put_row<D>(f[u], p.signs, false, y >= wk.Lq && y < wk.L ? sk : nullptr, kKeyPitch,
-                                       slot_of(s, vn), kn);
+                            put_row<D>(f[u], p.signs, false, y >= wk.Lq && y < wk.L ? sk : nullptr, kKeyPitch, slot_of(s, vn), kn);
                         }
                     }
                 }
-                if (i == 0) {
-                    int hidden = 0;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (pg[e] < 0 && t0 + e * kPage < wk.Lq) hidden |= 1 << e;
-                    sm.hidden[j & 3] = hidden;
-                }
+                if (i == 0) sm.hidden[j & 7] = pg < 0 && t0 < wk.Lq;
                 fence_proxy_async();
                 arrive(&sm.kfull[st]);
-                pg[0] = pg_next[0];
-                pg[1] = pg_next[1];
-                present(pg);
-                load(pg);
-                pages(j + 2, pg_next);
+                pg = present(pg_next);
+                load();
+                pg_next = page_of(j + 2);
             }
         } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
             const int i = threadIdx.x - 384, vrun = p.vchan_bytes;
-            const int ch = i & (D - 1), gi = ch / p.vg, vp = (i / D) & 1;    // page of the tile
+            const int ch = i & (D - 1), gi = ch / p.vg, half = (i / D) & 1;  // channel, half of the positions
             const bool active = i < 2 * D;
-            const int position = i & 127, g0 = i >> 7;    // metadata: position, groups g0, g0 + 2, ...
+            const int position = i & 63, g0 = i >> 6;     // metadata: position, groups g0 and g0 + 4
             const int at = slot_of(position, vn);
-            uint4 raw[4];
-            uint32_t meta[4];
-            auto load = [&](const int (&g2)[2], int j) {
-                const int ph = vp ? g2[1] : g2[0];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) raw[c] = make_uint4(0, 0, 0, 0);
-                if (ph >= 0 && active)
-                    load_pieces<4>(raw, p.v_codes + (size_t(ph) * p.hkv + wk.h) * size_t(D) * vrun + ch * p.vch, D * 16, vrun);
-                const int pm = position >> 6 ? g2[1] : g2[0], y = j < wk.n_tile ? wk.tile_start(j) + position : 0;
-                const bool have = pm >= 0 && y < wk.Lq && wk.used(y);
-                const uint32_t* m = p.v_meta + ((size_t(max(pm, 0)) * p.hkv + wk.h) * kPage + (position & 63)) * p.nvg;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (g0 + 2 * e < p.nvg) meta[e] = have ? __ldg(m + g0 + 2 * e) : 0u;
+            uint4 raw[2];
+            uint32_t meta[2];
+            const size_t code_step = size_t(p.hkv) * D * vrun, meta_step = size_t(p.hkv) * kPage * p.nvg;
+            const uint8_t* codes = p.v_codes + size_t(wk.h) * D * vrun + ch * p.vch + part_offset(half * (vrun / 2), p.vch, D * 16);
+            const uint32_t* metas = p.v_meta + (size_t(wk.h) * kPage + position) * p.nvg + g0;
+            auto load = [&](int j) {
+                raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
+                meta[0] = meta[1] = 0;
+                if (pg < 0) return;
+                if (active) load_part<2>(raw, codes + pg * code_step, D * 16, vrun / 2);
+                const int y = wk.tile_start(j) + position;
+                if (g0 < p.nvg && y < wk.Lq && wk.used(y)) {
+                    const uint32_t* m = metas + pg * meta_step;
+                    meta[0] = __ldg(m);
+                    if (g0 + 4 < p.nvg) meta[1] = __ldg(m + 4);
+                }
             };
-            load(pg, 0);
+            load(0);
+#pragma unroll 1
             for (int j = 0; j < wk.n_tile; ++j) {
-                const int st = j & 1, y0 = wk.tile_start(j) + vp * kPage;
+                const int st = j % kStages, y0 = wk.tile_start(j) + half * 32;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (g0 + 2 * e < p.nvg) {
-                        sm.vscale[st][g0 + 2 * e][at] = __ushort_as_half(uint16_t(meta[e]));
-                        sm.vzero[st][g0 + 2 * e][at] = __ushort_as_half(uint16_t(meta[e] >> 16));
+                for (int e = 0; e < 2; ++e)
+                    if (g0 + 4 * e < p.nvg) {
+                        sm.vscale[j & 1][g0 + 4 * e][at] = __ushort_as_half(uint16_t(meta[e]));
+                        sm.vzero[j & 1][g0 + 4 * e][at] = __ushort_as_half(uint16_t(meta[e] >> 16));
                     }
-                if (j >= kStages) ok = wait(&sm.vempty[st], ((j >> 1) + 1) & 1);
+                if (j >= kStages) ok = wait(&sm.vempty[st], (j / kStages + 1) & 1);
                 {   // the metadata is there (the other tile's may still be read); and do all the warps go on?
                     uint32_t all;
                     asm volatile(
@@ -864,34 +842,83 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                     ok = all != 0;
                     if (!ok) break;
                 }
-                unsigned char* to = sm.v[st] + ch * 16;
                 if (active) {
-                    if (p.vb == 2) put_value<2, D>(sm, st, raw, gi, vp, to);
-                    if (p.vb == 4) put_value<4, D>(sm, st, raw, gi, vp, to);
-                    if (p.vb == 8) put_value<8, D>(sm, st, raw, gi, vp, to);
-                    if (p.vb == 1) put_value<1, D>(sm, st, raw, gi, vp, to);
-                    if (y0 + kPage > wk.Lq) {             // ring positions (the page's codes gave zeros there)
+                    unsigned char* to = sm.v[st] + ch * 16 + half * 4 * (D * 16);
+                    const __half *vs = &sm.vscale[j & 1][gi][half * 32], *vz = &sm.vzero[j & 1][gi][half * 32];
+                    if (p.vb == 2) put_value<2, D>(vs, vz, raw, to);
+                    if (p.vb == 4) put_value<4, D>(vs, vz, raw, to);
+                    if (p.vb == 8) put_value<8, D>(vs, vz, raw, to);
+                    if (p.vb == 1) put_value<1, D>(vs, vz, raw, to);
+                    if (y0 + 32 > wk.Lq) {                // ring positions (the page's codes gave zeros there)
                         const __nv_bfloat16* win = p.v_win + (size_t(wk.b) * p.hkv + wk.h) * R * D + ch;
-                        if (p.vb == 2) put_ring_value<16, D>(wk, win, R, y0, vp, to);
-                        if (p.vb == 4) put_ring_value<8, D>(wk, win, R, y0, vp, to);
-                        if (p.vb == 8) put_ring_value<4, D>(wk, win, R, y0, vp, to);
-                        if (p.vb == 1) put_ring_value<32, D>(wk, win, R, y0, vp, to);
+                        if (p.vb == 2) put_ring_value<16, D>(wk, win, R, y0, to);
+                        if (p.vb == 4) put_ring_value<8, D>(wk, win, R, y0, to);
+                        if (p.vb == 8) put_ring_value<4, D>(wk, win, R, y0, to);
+                        if (p.vb == 1) put_ring_value<32, D>(wk, win, R, y0, to);
                     }
                 }
                 fence_proxy_async();
                 arrive(&sm.vfull[st]);
-                pg[0] = pg_next[0];
-                pg[1] = pg_next[1];
-                present(pg);
-                load(pg, j + 1);
-                pages(j + 2, pg_next);
+                pg = present(pg_next);
+                load(j + 1);
+                pg_next = page_of(j + 2);
+            }
+        }
+    } else {
+        // ------------------------------------------------ products
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (warp == 20 && wk.n_tile > 0 && elected()) {   // one thread: a tile's hand-overs cost it a dozen instructions
+            constexpr uint32_t kS = idesc_f16(kRows, kTile), kO = idesc_f16(kRows, D);
+            const uint64_t qd = smem_desc(smem_u32(sm.q[0]), kQueryPitch, 128);
+            const uint64_t kd = smem_desc(smem_u32(sm.k[0]), kKeyPitch, 128), vd = smem_desc(smem_u32(sm.v[0]), D * 16, 128);
+            constexpr int kQStep = int(sizeof(sm.q[0])) >> 4, kKStep = int(sizeof(sm.k[0])) >> 4, kVStep = int(sizeof(sm.v[0])) >> 4;
+            auto reached = [&](uint64_t* bar, int parity) -> bool {
+                const uint32_t at = smem_u32(bar);
+                return mbar_try_wait(at, uint32_t(parity)) || late(at, parity);
+            };
+            const int last = two ? 1 : 0;
+            bool ok = true;
+            // S of the first two tiles, then for each tile and block: O += P V, S of the tile after the next
+#pragma unroll 1
+            for (int j = -2; j < wk.n_tile && ok; ++j) {
+                const int ahead = j + 2, vs = j & (kStages - 1), ks = ahead & (kStages - 1);
+#pragma unroll 1
+                for (int m = 0; m <= last; ++m) {
+                    const uint32_t tile = tmem + (m * 2 + (j & 1)) * kTile;
+                    if (j >= 0) {
+                        ok = (m > 0 || reached(&sm.vfull[vs], (j / kStages) & 1)) && reached(&sm.pfull[m][j & 1], (j >> 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t v = vd + uint64_t(vs * kVStep);
+                        const uint32_t d = tmem + 256 + m * D;
+                        if (j == 0)
+                            mma_ts<false>(d, tile, v, kO);
+                        else
+                            mma_ts<true>(d, tile, v, kO);
+#pragma unroll
+                        for (int s = 1; s < kTile / 16; ++s) mma_ts<true>(d, tile + s * 8, v + s * (2 * D * 16 >> 4), kO);
+                        commit(&sm.odone[m]);
+                        if (j + 1 == wk.n_tile) commit(&sm.olast[m]);
+                        if (m == last) commit(&sm.vempty[vs]);
+                    }
+                    if (ahead >= wk.n_tile) continue;
+                    if (m == 0) ok = reached(&sm.kfull[ks], (ahead / kStages) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t q = qd + uint64_t(m * kQStep), k = kd + uint64_t(ks * kKStep);
+                    mma_ss<false>(tile, q, k, kS);
+#pragma unroll
+                    for (int s = 1; s < D / 16; ++s) mma_ss<true>(tile, q + s * (2 * kQueryPitch >> 4), k + s * (2 * kKeyPitch >> 4), kS);
+                    commit(&sm.sfull[m][j & 1]);
+                    if (m == last) commit(&sm.kempty[ks]);
+                }
             }
         }
     }
     // every product has been waited for by the weights' warps, or the waits have given up
     tc_fence_before();
     __syncthreads();
-    if (warp == 15) tmem_dealloc(tmem, 512);
+    if (warp == 20) tmem_dealloc(tmem, 512);
 }
 
 template <int D>
