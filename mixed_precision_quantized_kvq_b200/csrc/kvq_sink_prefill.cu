@@ -24,7 +24,7 @@
 //              (groups along positions: two channels of half the positions).
 //   12-19      values: thread = half the positions of a channel.  Codes and
 //              metadata are loaded a tile ahead, page numbers two.
-//   20         issues the products (21-23 fill its warp group).
+//   20, 21     issue the products of block 0 and 1 (22, 23 fill the warp group).
 // The kernel is launched with 80 registers a thread, 1920 over its 24 warps; the
 // roles then take 96, 112, 64 and 48: 8*96 + 4*112 + 8*64 + 4*48 = 1920.
 // Operands are 8x16-byte core matrices without swizzle, all 16-byte pieces of
@@ -70,10 +70,9 @@ struct Smem {
     unsigned char v[kStages][kV];
     alignas(16) __half vscale[2][8][kTile];             // value scales and zero points of two tiles: by group, in the
     alignas(16) __half vzero[2][8][kTile];              // order of the unpacked codes
-    float factor[2][kRows];
     uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
     uint64_t sfull[2][2], pfull[2][2];                  // block, tile % 2
-    uint64_t odone[2], olast[2];                        // a tile's values, the last tile's
+    uint64_t odone[2], olast[2], qfull[2];              // a tile's values, the last tile's; the queries
     uint32_t tmem;
     int hidden[8];                                      // tile % 8: its page is absent
     int failed;
@@ -151,11 +150,6 @@ __device__ __forceinline__ void tmem_loaded(uint32_t (&r)[32]) {
                  :
                  : "memory");
     asm volatile("" : "+r"(r[30]), "+r"(r[31]) : : "memory");
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t v;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-    return v;
 }
 __device__ __forceinline__ void arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -390,6 +384,50 @@ __device__ __forceinline__ void put_ring_key(const __nv_bfloat16* src, unsigned 
     }
 }
 
+// One query row (zeros where `have` is false) to its row of the queries, in the channel order of words of N codes, times
+// `sign` and a power of two that brings its largest element into [2^13, 2^14); returns that power's inverse.  The row is
+// read twice, the second time from the cache.
+template <int N, int D>
+__device__ __forceinline__ float put_query(const void* q, bool bf16, bool have, size_t at, float sign, unsigned char* to) {
+    constexpr int C = N > 8 ? N : 8;                     // channels that are exchanged among themselves
+    float m = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D; c += 8) {
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (have) load8(q, bf16, at + c, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+    }
+    const int e = max(-100, int(__float_as_uint(m) >> 23) - 127);
+    const float up = sign * __uint_as_float(uint32_t(127 + 13 - e) << 23);
+#pragma unroll 2
+    for (int c = 0; c < D; c += C) {
+        float x[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) x[i] = 0.f;
+        if (have) {
+#pragma unroll
+            for (int k = 0; k < C / 8; ++k) {
+                float y[8];
+                load8(q, bf16, at + c + 8 * k, y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[8 * k + i] = y[i];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < C / 8; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int low = pair_low<N>(4 * k + i);
+                w[i] = bits(__floats2half2_rn(x[low] * up, x[low + N / 2] * up));
+            }
+            *reinterpret_cast<uint4*>(to + (c / 8 + k) * kQueryPitch) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    return __uint_as_float(uint32_t(127 - 13 + e) << 23);
+}
+
 // ---------------------------------------------------------------- values
 
 // half a channel's run of a page to the value tile: pieces of eight slots, D*16 bytes apart
@@ -493,8 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sm.kfull[i], kKeyThreads);
             mbar_init(&sm.vfull[i], kValueThreads);
-            mbar_init(&sm.kempty[i], 1);
-            mbar_init(&sm.vempty[i], 1);
+            mbar_init(&sm.kempty[i], two ? 2 : 1);        // a commit of each block
+            mbar_init(&sm.vempty[i], two ? 2 : 1);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&sm.sfull[i >> 1][i & 1], 1);
@@ -504,6 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
         mbar_init(&sm.odone[1], 1);
         mbar_init(&sm.olast[0], 1);
         mbar_init(&sm.olast[1], 1);
+        mbar_init(&sm.qfull[0], kRows);
+        mbar_init(&sm.qfull[1], kRows);
         sm.failed = 0;
         mbar_fence_init();
     }
@@ -511,33 +551,6 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
         tmem_alloc(&sm.tmem, 512);
         tmem_relinquish();
     }
-    {   // queries
-        constexpr int kPer = 32 / (D / 8);
-        const float scale = fabsf(a.scale_log2), sign = a.scale_log2 < 0.f ? -1.f : 1.f;
-#pragma unroll 1
-        for (int r0 = warp * (4 * kPer); r0 < 2 * kRows; r0 += kThreads / 32 * (4 * kPer)) {   // four loads under way
-            const int oct = lane % (D / 8);
-            float x[4][8];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int rr = r0 + u * kPer + lane / (D / 8), m = rr / kRows, r = rr % kRows, qi = m * QT + r / g;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-                if (r < QT * g && qi < nq)
-                    load8(a.q, a.q_bf16, (sq.row + i0 + qi) * a.q_stride + size_t(wk.h * g + r % g) * D + oct * 8, x[u]);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int rr = r0 + u * kPer + lane / (D / 8), m = rr / kRows, r = rr % kRows;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[u][i] *= sign;
-                const float down = put_row<D>(x[u], p.rotate ? p.signs : nullptr, true, sm.q[m], kQueryPitch, r, kn);
-                // (never zero: -inf times it has to stay -inf)
-                if (oct == 0) sm.factor[m][r] = fmaxf(scale * down, 1e-37f);
-            }
-        }
-    }
-    fence_proxy_async();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -570,8 +583,52 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
         if (m == 0 || two) {
             const uint32_t lanes = uint32_t(warp & 3) * 32u << 16;
             const uint32_t to = tmem + 256 + m * D + lanes;
-            const float factor = sm.factor[m][r];
             const int q_in = r / g;
+            // ---- queries, while the first tiles come in ----
+            const float scale = fabsf(a.scale_log2), sign = a.scale_log2 < 0.f ? -1.f : 1.f;
+            float factor;
+            if (!p.rotate) {                              // this thread's row
+                const bool have = r < QT * g && m * QT + q_in < nq;
+                const size_t at = (sq.row + i0 + m * QT + q_in) * a.q_stride + size_t(wk.h * g + r % g) * D;
+                unsigned char* to = sm.q[m] + r * 16;
+                float down = 1.f;
+                if (kn == 8) down = put_query<8, D>(a.q, a.q_bf16, have, at, sign, to);
+                if (kn == 2) down = put_query<2, D>(a.q, a.q_bf16, have, at, sign, to);
+                if (kn == 4) down = put_query<4, D>(a.q, a.q_bf16, have, at, sign, to);
+                if (kn == 16) down = put_query<16, D>(a.q, a.q_bf16, have, at, sign, to);
+                if (kn == 32) down = put_query<32, D>(a.q, a.q_bf16, have, at, sign, to);
+                factor = scale * down;
+            } else {                                      // the warp's rows, D/8 lanes each, four loads under way
+                constexpr int kPer = 32 / (D / 8);
+                const int oct = lane % (D / 8), first = r - lane;
+                factor = 0.f;
+#pragma unroll 1
+                for (int r0 = 0; r0 < 32; r0 += 4 * kPer) {
+                    float x[4][8];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int rr = first + r0 + u * kPer + lane / (D / 8), qi = m * QT + rr / g;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+                        if (rr < QT * g && qi < nq)
+                            load8(a.q, a.q_bf16, (sq.row + i0 + qi) * a.q_stride + size_t(wk.h * g + rr % g) * D + oct * 8, x[u]);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int rr = first + r0 + u * kPer + lane / (D / 8);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[u][i] *= sign;
+                        const float down = put_row<D>(x[u], p.signs, true, sm.q[m], kQueryPitch, rr, kn);
+                        // to the lane whose row it is
+                        const int from = lane - r0 - u * kPer;
+                        const float v = __shfl_sync(0xffffffffu, down, from >= 0 && from < kPer ? from * (D / 8) : 0);
+                        if (from >= 0 && from < kPer) factor = scale * v;
+                    }
+                }
+            }
+            factor = fmaxf(factor, 1e-37f);               // (never zero: -inf times it has to stay -inf)
+            fence_proxy_async();
+            arrive(&sm.qfull[m]);
             const int t = sq.base + i0 + m * QT + min(q_in, QT - 1);
             const int t_first = sq.base + i0 + m * QT, t_last = min(t_first + QT - 1, wk.p_max);
             float ref = kRefNone, l = 0.f;
@@ -633,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                     }
                 }
                 const uint64_t f2 = pack2(factor, factor), r2 = pack2(-ref, -ref);
-                uint64_t part[4] = {0, 0, 0, 0};
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     uint32_t* q = &s[i >> 4][2 * (i & 15)];
@@ -641,15 +698,11 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                     unpack2(fma2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), f2, r2), x, y);
                     x = ex2(x);
                     y = ex2(y);
-                    part[i & 3] = add2(part[i & 3], pack2(x, y));
+                    part[i & 3] += x + y;
                     s[0][i] = bits(__floats2half2_rn(x, y));   // (slot i has been read)
                 }
                 tmem_st32(ts, s[0]);                      // over S
-                {
-                    float x, y;
-                    unpack2(add2(add2(part[0], part[1]), add2(part[2], part[3])), x, y);
-                    l += x + y;
-                }
+                l += (part[0] + part[1]) + (part[2] + part[3]);
                 tc_wait_st();
                 tc_fence_before();
                 arrive(&sm.pfull[m][j & 1]);
@@ -867,51 +920,50 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
     } else {
         // ------------------------------------------------ products
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        if (warp == 20 && wk.n_tile > 0 && elected()) {   // one thread: a tile's hand-overs cost it a dozen instructions
+        const int m = warp - 20;
+        // One thread a block (two warps, so two schedulers): a hand-over then costs a dozen instructions, and the
+        // instructions around a product, not the tensor core, are what limits a thread.
+        if (m < (two ? 2 : 1) && wk.n_tile > 0 && elected()) {
             constexpr uint32_t kS = idesc_f16(kRows, kTile), kO = idesc_f16(kRows, D);
-            const uint64_t qd = smem_desc(smem_u32(sm.q[0]), kQueryPitch, 128);
+            const uint64_t qd = smem_desc(smem_u32(sm.q[m]), kQueryPitch, 128);
             const uint64_t kd = smem_desc(smem_u32(sm.k[0]), kKeyPitch, 128), vd = smem_desc(smem_u32(sm.v[0]), D * 16, 128);
-            constexpr int kQStep = int(sizeof(sm.q[0])) >> 4, kKStep = int(sizeof(sm.k[0])) >> 4, kVStep = int(sizeof(sm.v[0])) >> 4;
+            constexpr int kKStep = int(sizeof(sm.k[0])) >> 4, kVStep = int(sizeof(sm.v[0])) >> 4;
+            const uint32_t d = tmem + 256 + m * D;
             auto reached = [&](uint64_t* bar, int parity) -> bool {
                 const uint32_t at = smem_u32(bar);
                 return mbar_try_wait(at, uint32_t(parity)) || late(at, parity);
             };
-            const int last = two ? 1 : 0;
-            bool ok = true;
-            // S of the first two tiles, then for each tile and block: O += P V, S of the tile after the next
+            bool ok = reached(&sm.qfull[m], 0);
+            // S of the first two tiles, then for each tile: O += P V, S of the tile after the next
 #pragma unroll 1
             for (int j = -2; j < wk.n_tile && ok; ++j) {
                 const int ahead = j + 2, vs = j & (kStages - 1), ks = ahead & (kStages - 1);
-#pragma unroll 1
-                for (int m = 0; m <= last; ++m) {
-                    const uint32_t tile = tmem + (m * 2 + (j & 1)) * kTile;
-                    if (j >= 0) {
-                        ok = (m > 0 || reached(&sm.vfull[vs], (j / kStages) & 1)) && reached(&sm.pfull[m][j & 1], (j >> 1) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t v = vd + uint64_t(vs * kVStep);
-                        const uint32_t d = tmem + 256 + m * D;
-                        if (j == 0)
-                            mma_ts<false>(d, tile, v, kO);
-                        else
-                            mma_ts<true>(d, tile, v, kO);
-#pragma unroll
-                        for (int s = 1; s < kTile / 16; ++s) mma_ts<true>(d, tile + s * 8, v + s * (2 * D * 16 >> 4), kO);
-                        commit(&sm.odone[m]);
-                        if (j + 1 == wk.n_tile) commit(&sm.olast[m]);
-                        if (m == last) commit(&sm.vempty[vs]);
-                    }
-                    if (ahead >= wk.n_tile) continue;
-                    if (m == 0) ok = reached(&sm.kfull[ks], (ahead / kStages) & 1);
+                const uint32_t tile = tmem + (m * 2 + (j & 1)) * kTile;
+                if (j >= 0) {
+                    ok = reached(&sm.vfull[vs], (j / kStages) & 1) && reached(&sm.pfull[m][j & 1], (j >> 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t q = qd + uint64_t(m * kQStep), k = kd + uint64_t(ks * kKStep);
-                    mma_ss<false>(tile, q, k, kS);
+                    const uint64_t v = vd + uint64_t(vs * kVStep);
+                    if (j == 0)
+                        mma_ts<false>(d, tile, v, kO);
+                    else
+                        mma_ts<true>(d, tile, v, kO);
 #pragma unroll
-                    for (int s = 1; s < D / 16; ++s) mma_ss<true>(tile, q + s * (2 * kQueryPitch >> 4), k + s * (2 * kKeyPitch >> 4), kS);
-                    commit(&sm.sfull[m][j & 1]);
-                    if (m == last) commit(&sm.kempty[ks]);
+                    for (int s = 1; s < kTile / 16; ++s) mma_ts<true>(d, tile + s * 8, v + s * (2 * D * 16 >> 4), kO);
+                    commit(&sm.odone[m]);
+                    if (j + 1 == wk.n_tile) commit(&sm.olast[m]);
+                    commit(&sm.vempty[vs]);
                 }
+                if (ahead >= wk.n_tile) continue;
+                ok = reached(&sm.kfull[ks], (ahead / kStages) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t k = kd + uint64_t(ks * kKStep);
+                mma_ss<false>(tile, qd, k, kS);
+#pragma unroll
+                for (int s = 1; s < D / 16; ++s) mma_ss<true>(tile, qd + s * (2 * kQueryPitch >> 4), k + s * (2 * kKeyPitch >> 4), kS);
+                commit(&sm.sfull[m][j & 1]);
+                commit(&sm.kempty[ks]);
             }
         }
     }
