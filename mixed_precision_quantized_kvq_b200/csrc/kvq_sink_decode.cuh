@@ -18,7 +18,7 @@
 // a kv-head as its 8 columns: fragments are registers, the codes never go
 // through shared memory a second time.
 //
-// Work split: one cluster of 1 to 8 CTAs per (sequence, kv-head); its warps
+// Work split: one cluster of 1 to 16 CTAs per (sequence, kv-head); its warps
 // take the 64-position pages in turn (warp w of W: pages w, w + W, ...), then
 // 16-slot pieces of the bf16 ring, each with its own buffers for keys and
 // values filled by cp.async.  The warps' partial sums meet in
@@ -790,26 +790,34 @@ __global__ void __launch_bounds__(kMaxWarps * 32) sink_decode_kernel(const __gri
     cl.sync();
     for (int e = rank * blockDim.x + threadIdx.x; e < p.g * (D / 2); e += ctas * blockDim.x) {
         const int x = e / (D / 2);
-        float ref[8], sum[8];
-        float2 v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const unsigned char* at = cl.map_shared_rank(smem, i < ctas ? i : 0);
-            const Head<D>& other = *reinterpret_cast<const Head<D>*>(at);
-            ref[i] = i < ctas ? other.factor[x] : kRefNone;
-            sum[i] = i < ctas ? other.qsum[x][0] : 0.f;
-            v[i] = i < ctas ? reinterpret_cast<const float2*>(at + sizeof(Head<D>))[e] : make_float2(0.f, 0.f);
-        }
-        float top = ref[0], l = 0.f;
-#pragma unroll
-        for (int i = 1; i < 8; ++i) top = fmaxf(top, ref[i]);
+        float top = kRefNone, l = 0.f;
         float2 o = make_float2(0.f, 0.f);
+        for (int c0 = 0; c0 < ctas; c0 += 8) {           // eight CTAs' parts under way at a time
+            float ref[8], sum[8];
+            float2 v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float f = ex2(ref[i] - top);
-            l = fmaf(sum[i], f, l);
-            o.x = fmaf(v[i].x, f, o.x);
-            o.y = fmaf(v[i].y, f, o.y);
+            for (int i = 0; i < 8; ++i) {
+                const bool have = c0 + i < ctas;
+                const unsigned char* at = cl.map_shared_rank(smem, have ? c0 + i : 0);
+                const Head<D>& other = *reinterpret_cast<const Head<D>*>(at);
+                ref[i] = have ? other.factor[x] : kRefNone;
+                sum[i] = have ? other.qsum[x][0] : 0.f;
+                v[i] = have ? reinterpret_cast<const float2*>(at + sizeof(Head<D>))[e] : make_float2(0.f, 0.f);
+            }
+            const float before = top;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, ref[i]);
+            const float f0 = ex2(before - top);
+            l *= f0;
+            o.x *= f0;
+            o.y *= f0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float f = ex2(ref[i] - top);
+                l = fmaf(sum[i], f, l);
+                o.x = fmaf(v[i].x, f, o.x);
+                o.y = fmaf(v[i].y, f, o.y);
+            }
         }
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const size_t row = size_t(b) * p.hq + h * p.g + x;
@@ -823,10 +831,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32) sink_decode_kernel(const __gri
 
 // CTAs per (sequence, kv-head).  A CTA of a round costs about its items (pages or ring pieces, shared by its warps)
 // plus one and a half for its start and its end; the rounds are what `slots` CTAs at a time make of all of them.
-inline int split_ctas(long long pairs, int items, int warps, int slots) {
+inline int split_ctas(long long pairs, int items, int warps, int slots, int most) {
     int best = 1;
     double least = 1e30;
-    for (int n = 1; n <= 8; ++n) {
+    for (int n = 1; n <= most; ++n) {
         if (n > 1 && n * warps > items) break;
         const double rounds = double((pairs * n + slots - 1) / slots);
         const double cost = rounds * (double((items + n * warps - 1) / (n * warps)) + 1.5);
@@ -841,14 +849,32 @@ inline int split_ctas(long long pairs, int items, int warps, int slots) {
 template <int D, int KB, int VB, bool LO>
 cudaError_t launch_decode_one(const Params& p, const Args& a, int sms, cudaStream_t s) {
     auto* kernel = sink_decode_kernel<D, KB, VB, LO>;
-    static int opted[64];                               // largest dynamic shared memory asked for, per device
+    // per device, once: large shared memory, and the largest cluster that fits at it (16 is beyond what every device
+    // has to offer, 8 is not)
+    static int largest[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     constexpr int kMost = 227 * 1024;
-    if (!opted[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (!largest[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
-        opted[dev] = kMost;
+        cudaLaunchConfig_t c{};
+        cudaLaunchAttribute at{};
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = 16;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        c.gridDim = dim3(16);
+        c.blockDim = dim3(256);
+        c.dynamicSmemBytes = kMost;
+        c.attrs = &at;
+        c.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &c) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        largest[dev] = n > 0 ? 16 : 8;
     }
     // four warps a CTA, or as many up to eight as bring the most warps onto an SM (large buffers)
     int warps = 4, per_sm = 1;
@@ -863,7 +889,7 @@ cudaError_t launch_decode_one(const Params& p, const Args& a, int sms, cudaStrea
     const int smem = decode_smem<D, KB, VB>(p, warps);
     const long long bound = std::min<long long>(a.len_cap, (long long)a.sinks + a.span + 2 * kPage);
     const int items = int((bound + kPage - 1) / kPage) + (std::min(p.W, a.len_cap) + kRing - 1) / kRing;
-    const int n = split_ctas((long long)p.batch * p.hkv, items, warps, sms * per_sm);
+    const int n = split_ctas((long long)p.batch * p.hkv, items, warps, sms * per_sm, largest[dev]);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(n, p.hkv, p.batch);
     cfg.blockDim = dim3(32 * warps);
