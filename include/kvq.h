@@ -193,7 +193,8 @@ int kvq_get_decode_path(const kvq_layout* layout);
 
 /* Decode diagnostics of the current device, counted by the decode kernels
  * since the library was loaded (or last cleared):
- *   wait_timeouts  bounded waits inside a decode kernel that gave up (the
+ *   wait_timeouts  bounded waits inside a decode kernel or inside
+ *                  kvq_sink_prefill_attention's that gave up (the
  *                  kernel then writes NaN for the outputs it could not
  *                  finish; 0 in normal operation)
  *   bad_tickets    merge tickets found above their count, i.e. a workspace

@@ -374,8 +374,14 @@ def _need_rows(q, name: str, rows: Optional[int], heads: int, d: int):
     return q.data_ptr(), _dtype_code(q), shape[0], stride[0] if shape[0] > 1 else heads * d, dev
 
 
+# the current stream's handle without a torch.cuda.Stream around it, where torch has it
+_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_of(stream, dev: int):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if stream is None and _RAW_STREAM is not None:
+        return _RAW_STREAM(dev)
+    return _stream(stream)
 
 
 def kvq_sink_decode_attention(layout: Layout, cache: PagedCache, q: torch.Tensor, lens: torch.Tensor, max_len: int,
@@ -401,6 +407,8 @@ def kvq_sink_prefill_attention(layout: Layout, cache: PagedCache, q: torch.Tenso
     positions up to each query -> out bf16 [total_q][Hq][d], lse fp32 [total_q][Hq]."""
     B, Hq, d = cache.batch, layout.num_q_heads, layout.head_dim
     qp, qt, T, stride, dev = _need_rows(q, "q", None, Hq, d)
+    if T == 0:                                   # nothing to do (an empty tensor has no address)
+        return
     rc = lib().kvq_sink_prefill_attention(
         C.byref(layout.c()), C.byref(cache.c()), qp, qt, stride, _need(cu_q, "cu_q", _I32, B + 1, dev),
         _need(lens, "lens", _I32, B, dev), int(max_q), int(sinks), int(span), sm_scale,
@@ -418,6 +426,8 @@ def kvq_read_back(layout: Layout, cache: PagedCache, first: torch.Tensor, cu_row
         raise ValueError("k_out and v_out must share a dtype")
     n = k_out.numel()
     dev = torch.cuda.current_device() if k_out.is_cuda else -1
+    if n == 0 and v_out.numel() == 0:            # nothing to do (an empty tensor has no address)
+        return
     if n % row:
         raise ValueError(f"k_out must hold whole rows of {row} elements ([rows][Hkv][d])")
     kp, vp = _need(k_out, "k_out", _FLOAT_IN, n, dev), _need(v_out, "v_out", _FLOAT_IN, n, dev)

@@ -38,6 +38,8 @@
 #include "kvq_sink.cuh"
 #include "kvq_tc_ptx.cuh"
 
+#include "kvq_mma_ptx.cuh"
+
 namespace kvq {
 namespace sink {
 namespace {
@@ -203,12 +205,22 @@ struct Work {
     __device__ __forceinline__ bool used(int x) const { return x <= p_max && (x < sinks || x >= lo); }
 };
 
+// eight bf16 numbers as fp32
+__device__ __forceinline__ void widen(const uint4& w, float (&x)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+
 // One row of D channels by D/8 neighbouring lanes, eight channels each, to column `row` of an operand of fp16 pieces
-// `pitch` bytes apart; n: codes per word of the keys (channel order).  scaled: by a power of two into [2^13, 2^14);
-// returns that power's inverse.  The whole warp calls it; nothing is stored where `to` is null.
+// `pitch` bytes apart; n: codes per word of the keys (channel order).  scaled: by `sign` and a power of two into
+// [2^13, 2^14); returns that power's inverse.  The whole warp calls it; nothing is stored where `to` is null.
 template <int D>
-__device__ __forceinline__ float put_row(float (&x)[8], const int8_t* signs, bool scaled, unsigned char* to, int pitch, int row,
-                                         int n) {
+__device__ __forceinline__ float put_row(float (&x)[8], const int8_t* signs, bool scaled, float sign, unsigned char* to,
+                                         int pitch, int row, int n) {
     const int oct = threadIdx.x % (D / 8);
     if (signs) {
 #pragma unroll
@@ -240,26 +252,29 @@ __device__ __forceinline__ float put_row(float (&x)[8], const int8_t* signs, boo
 #pragma unroll
         for (int w = 1; w < D / 8; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
         const int e = max(-100, int(__float_as_uint(m) >> 23) - 127);
-        up = __uint_as_float(uint32_t(127 + 13 - e) << 23);
+        up = sign * __uint_as_float(uint32_t(127 + 13 - e) << 23);
         down = __uint_as_float(uint32_t(127 - 13 + e) << 23);
     }
+    if (!to) return down;
+    if (n <= 8) {                                        // the lane's channels stay in one piece
+        const auto pair = [&](int a, int b) { return bits(__floats2half2_rn(x[a] * up, x[b] * up)); };
+        *reinterpret_cast<uint4*>(to + oct * pitch + row * 16) =
+            n == 8   ? make_uint4(pair(0, 4), pair(1, 5), pair(2, 6), pair(3, 7))
+            : n == 4 ? make_uint4(pair(0, 2), pair(1, 3), pair(4, 6), pair(5, 7))
+                     : make_uint4(pair(0, 1), pair(2, 3), pair(4, 5), pair(6, 7));
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int s = slot_of(oct * 8 + i, n);
-        if (to) *reinterpret_cast<__half*>(to + (s >> 3) * pitch + row * 16 + (s & 7) * 2) = __float2half_rn(x[i] * up);
+        for (int i = 0; i < 8; ++i) {
+            const int s = slot_of(oct * 8 + i, n);
+            *reinterpret_cast<__half*>(to + (s >> 3) * pitch + row * 16 + (s & 7) * 2) = __float2half_rn(x[i] * up);
+        }
     }
     return down;
 }
 
 __device__ __forceinline__ void load8(const void* src, bool bf16, size_t at, float (&x)[8]) {
     if (bf16) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(src) + at));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(u[i] << 16);
-            x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-        }
+        widen(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(src) + at)), x);
     } else {
         const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
         const float4 a = __ldg(f), b = __ldg(f + 1);
@@ -384,35 +399,29 @@ __device__ __forceinline__ void put_ring_key(const __nv_bfloat16* src, unsigned 
     }
 }
 
-// One query row (zeros where `have` is false) to its row of the queries, in the channel order of words of N codes, times
-// `sign` and a power of two that brings its largest element into [2^13, 2^14); returns that power's inverse.  The row is
-// read twice, the second time from the cache.
+// One bf16 query row, as it came to its place among the queries, to fp16 in the channel order of words of N codes, times
+// `sign` and a power of two that brings its largest element into [2^13, 2^14); returns that power's inverse.
 template <int N, int D>
-__device__ __forceinline__ float put_query(const void* q, bool bf16, bool have, size_t at, float sign, unsigned char* to) {
+__device__ __forceinline__ float turn_query(unsigned char* row, float sign) {
     constexpr int C = N > 8 ? N : 8;                     // channels that are exchanged among themselves
-    float m = 0.f;
+    uint32_t top = 0;                                    // largest magnitude, as bf16 bits in either half
 #pragma unroll 4
-    for (int c = 0; c < D; c += 8) {
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (have) load8(q, bf16, at + c, x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+    for (int k = 0; k < D / 8; ++k) {
+        const uint4 v = *reinterpret_cast<const uint4*>(row + k * kQueryPitch);
+        top = __vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
+        top = __vmaxu2(__vmaxu2(top, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
     }
-    const int e = max(-100, int(__float_as_uint(m) >> 23) - 127);
+    const int e = max(-100, int(max(top >> 16, top & 0xffffu) >> 7) - 127);
     const float up = sign * __uint_as_float(uint32_t(127 + 13 - e) << 23);
 #pragma unroll 2
-    for (int c = 0; c < D; c += C) {
+    for (int k0 = 0; k0 < D / 8; k0 += C / 8) {
         float x[C];
 #pragma unroll
-        for (int i = 0; i < C; ++i) x[i] = 0.f;
-        if (have) {
+        for (int k = 0; k < C / 8; ++k) {
+            float y[8];
+            widen(*reinterpret_cast<const uint4*>(row + (k0 + k) * kQueryPitch), y);
 #pragma unroll
-            for (int k = 0; k < C / 8; ++k) {
-                float y[8];
-                load8(q, bf16, at + c + 8 * k, y);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[8 * k + i] = y[i];
-            }
+            for (int i = 0; i < 8; ++i) x[8 * k + i] = y[i] * up;
         }
 #pragma unroll
         for (int k = 0; k < C / 8; ++k) {
@@ -420,9 +429,9 @@ __device__ __forceinline__ float put_query(const void* q, bool bf16, bool have, 
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int low = pair_low<N>(4 * k + i);
-                w[i] = bits(__floats2half2_rn(x[low] * up, x[low + N / 2] * up));
+                w[i] = bits(__floats2half2_rn(x[low], x[low + N / 2]));
             }
-            *reinterpret_cast<uint4*>(to + (c / 8 + k) * kQueryPitch) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(row + (k0 + k) * kQueryPitch) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
     return __uint_as_float(uint32_t(127 - 13 + e) << 23);
@@ -586,41 +595,48 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
             const int q_in = r / g;
             // ---- queries, while the first tiles come in ----
             const float scale = fabsf(a.scale_log2), sign = a.scale_log2 < 0.f ? -1.f : 1.f;
-            float factor;
-            if (!p.rotate) {                              // this thread's row
+            float factor = 0.f;
+            {
+                constexpr int kPer = 32 / (D / 8);        // rows of the warp at a time, D/8 lanes each
+                const int oct = lane % (D / 8), sub = lane / (D / 8), first = r - lane;
+                // each lane knows its own row's place (-1: no such row)
                 const bool have = r < QT * g && m * QT + q_in < nq;
-                const size_t at = (sq.row + i0 + m * QT + q_in) * a.q_stride + size_t(wk.h * g + r % g) * D;
-                unsigned char* to = sm.q[m] + r * 16;
-                float down = 1.f;
-                if (kn == 8) down = put_query<8, D>(a.q, a.q_bf16, have, at, sign, to);
-                if (kn == 2) down = put_query<2, D>(a.q, a.q_bf16, have, at, sign, to);
-                if (kn == 4) down = put_query<4, D>(a.q, a.q_bf16, have, at, sign, to);
-                if (kn == 16) down = put_query<16, D>(a.q, a.q_bf16, have, at, sign, to);
-                if (kn == 32) down = put_query<32, D>(a.q, a.q_bf16, have, at, sign, to);
-                factor = scale * down;
-            } else {                                      // the warp's rows, D/8 lanes each, four loads under way
-                constexpr int kPer = 32 / (D / 8);
-                const int oct = lane % (D / 8), first = r - lane;
-                factor = 0.f;
-#pragma unroll 1
-                for (int r0 = 0; r0 < 32; r0 += 4 * kPer) {
-                    float x[4][8];
+                const long long own =
+                    have ? (long long)(sq.row + i0 + m * QT + q_in) * a.q_stride + (long long)(wk.h * g + r % g) * D : -1ll;
+                if (a.q_bf16) {                           // as they are to their place, all under way at once
+                    const uint32_t to = smem_u32(sm.q[m]) + oct * kQueryPitch;
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int rr = first + r0 + u * kPer + lane / (D / 8), qi = m * QT + rr / g;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-                        if (rr < QT * g && qi < nq)
-                            load8(a.q, a.q_bf16, (sq.row + i0 + qi) * a.q_stride + size_t(wk.h * g + rr % g) * D + oct * 8, x[u]);
+                    for (int r0 = 0; r0 < 32; r0 += kPer) {
+                        const long long at = __shfl_sync(0xffffffffu, own, r0 + sub);
+                        cp16_zfill(to + (first + r0 + sub) * 16, static_cast<const __nv_bfloat16*>(a.q) + (at >= 0 ? at + oct * 8 : 0),
+                                   at >= 0);
                     }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int rr = first + r0 + u * kPer + lane / (D / 8);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) x[u][i] *= sign;
-                        const float down = put_row<D>(x[u], p.signs, true, sm.q[m], kQueryPitch, rr, kn);
-                        // to the lane whose row it is
-                        const int from = lane - r0 - u * kPer;
+                    cp_async_wait_all();
+                    __syncwarp();
+                }
+                if (a.q_bf16 && !p.rotate) {              // in place, each lane its row
+                    unsigned char* to = sm.q[m] + r * 16;
+                    float down = 1.f;
+                    if (kn == 8) down = turn_query<8, D>(to, sign);
+                    if (kn == 2) down = turn_query<2, D>(to, sign);
+                    if (kn == 4) down = turn_query<4, D>(to, sign);
+                    if (kn == 16) down = turn_query<16, D>(to, sign);
+                    if (kn == 32) down = turn_query<32, D>(to, sign);
+                    factor = scale * down;
+                } else {
+#pragma unroll 2
+                    for (int r0 = 0; r0 < 32; r0 += kPer) {
+                        const int rr = first + r0 + sub;
+                        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                        if (a.q_bf16) {
+                            widen(*reinterpret_cast<const uint4*>(sm.q[m] + oct * kQueryPitch + rr * 16), x);
+                        } else {
+                            const long long at = __shfl_sync(0xffffffffu, own, r0 + sub);
+                            if (at >= 0) load8(a.q, false, size_t(at) + oct * 8, x);
+                        }
+                        // (its exchanges come after every lane's read and before any lane's store)
+                        const float down = put_row<D>(x, p.rotate ? p.signs : nullptr, true, sign, sm.q[m], kQueryPitch, rr, kn);
+                        const int from = lane - r0;       // to the lane whose row it is
                         const float v = __shfl_sync(0xffffffffu, down, from >= 0 && from < kPer ? from * (D / 8) : 0);
                         if (from >= 0 && from < kPer) factor = scale * v;
                     }
@@ -838,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             const int s = s0 + u * kPer + lane / (D / 8), y = t0 + s;
-                            put_row<D>(f[u], p.signs, false, y >= wk.Lq && y < wk.L ? sk : nullptr, kKeyPitch, slot_of(s, vn), kn);
+                            put_row<D>(f[u], p.signs, false, 1.f, y >= wk.Lq && y < wk.L ? sk : nullptr, kKeyPitch, slot_of(s, vn), kn);
                         }
                     }
                 }
@@ -985,7 +1001,7 @@ cudaError_t launch_d(const Params& p, const Args& a, unsigned* status, cudaStrea
         opted[dev] = true;
     }
     const int per = 2 * (kRows / p.g);
-    const dim3 grid((a.max_q + per - 1) / per, p.hkv, p.batch);
+    const dim3 grid((a.max_q - 1) / per + 1, p.hkv, p.batch);
     sink_prefill_kernel<D><<<grid, kThreads, kBytes, s>>>(p, a, status);
     return cudaGetLastError();
 }
