@@ -8,7 +8,7 @@ cudaError_t launch_sink_decode_k2(const Params&, const sink::Args&, int, cudaStr
 cudaError_t launch_sink_decode_k4(const Params&, const sink::Args&, int, cudaStream_t);
 cudaError_t launch_sink_decode_k8(const Params&, const sink::Args&, int, cudaStream_t);
 namespace sink {
-cudaError_t launch_prefill(const Params&, const Args&, unsigned*, cudaStream_t);
+cudaError_t launch_prefill(const Params&, const Args&, int, unsigned*, cudaStream_t);
 }
 
 cudaError_t launch_sink_attention(const Params& p, const sink::Args& a, int sms, cudaStream_t s) {
@@ -23,7 +23,7 @@ cudaError_t launch_sink_attention(const Params& p, const sink::Args& a, int sms,
     }
     unsigned* status = status_words();
     if (!status) return cudaErrorInvalidSymbol;
-    return sink::launch_prefill(p, a, status, s);
+    return sink::launch_prefill(p, a, sms, status, s);
 }
 
 }  // namespace kvq

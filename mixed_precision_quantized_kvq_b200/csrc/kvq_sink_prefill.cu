@@ -27,6 +27,9 @@
 //   20, 21     issue the products of block 0 and 1 (22, 23 fill the warp group).
 // The kernel is launched with 80 registers a thread, 1920 over its 24 warps; the
 // roles then take 96, 112, 64 and 48: 8*96 + 4*112 + 8*64 + 4*48 = 1920.
+// Where few rows leave SMs idle and there are tiles enough, a cluster of 2, 4 or
+// 8 CTAs shares the tiles of its rows (CTA c of n: tiles c, c + n, ...) and joins
+// its outputs through distributed shared memory.
 // Operands are 8x16-byte core matrices without swizzle, all 16-byte pieces of
 // the same eight columns together, which makes the writers' 16-byte stores
 // contiguous over a warp.  A word holds the codes (i, i + n/2) in the same
@@ -34,6 +37,11 @@
 // sorting them, the query's channels are stored in the same order (keys), and
 // key rows, that is, the columns of S and P (values).
 #include <math.h>
+
+#include <algorithm>
+
+#include <cooperative_groups.h>
+#include <stddef.h>
 
 #include "kvq_sink.cuh"
 #include "kvq_tc_ptx.cuh"
@@ -107,6 +115,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 __device__ __forceinline__ void commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// floats between the rows of a CTA's part of a join: the output, reference, sum
+template <int D>
+constexpr int kPartPitch = D + 4;
+
 // instruction descriptor: fp16 A and B (K-major), fp32 accumulator
 constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24); }
 
@@ -196,11 +211,16 @@ __device__ __forceinline__ uint32_t slots_of(uint32_t v, int n) {
     return v;
 }
 
-// What a CTA works on.
+// What a CTA works on.  SPLIT: several CTAs share the tiles (the others' code does without).
+template <bool SPLIT>
 struct Work {
     int b, h, L, Lq, lo, p_max, sinks;          // lo: first position of the first query's span
-    int n_sink, first, n_tile;                  // tiles of the sinks, first tile of the span, all tiles
-    __device__ __forceinline__ int tile_start(int j) const { return (j < n_sink ? j : j - n_sink + first) * kTile; }
+    int n_sink, first, n_tile;                  // tiles of the sinks, first tile of the span, this CTA's tiles
+    int rank, ctas;                             // this CTA takes tiles rank, rank + ctas, ...
+    __device__ __forceinline__ int tile_start(int j) const {
+        if (SPLIT) j = j * ctas + rank;
+        return (j < n_sink ? j : j - n_sink + first) * kTile;
+    }
     // seen by some row (a necessary condition; the rows' own masks are exact)
     __device__ __forceinline__ bool used(int x) const { return x <= p_max && (x < sinks || x >= lo); }
 };
@@ -469,8 +489,8 @@ __device__ __forceinline__ void put_value(const __half* scale, const __half* zer
 }
 
 // one channel of the ring positions among 32 positions from y0 on, in the order of words of N codes
-template <int N, int D>
-__device__ __forceinline__ void put_ring_value(const Work& wk, const __nv_bfloat16* win, int R, int y0, unsigned char* to) {
+template <int N, int D, bool SPLIT>
+__device__ __forceinline__ void put_ring_value(const Work<SPLIT>& wk, const __nv_bfloat16* win, int R, int y0, unsigned char* to) {
     constexpr int C = N > 16 ? N : 16;                   // positions that are loaded at a time
 #pragma unroll 1
     for (int o0 = 0; o0 < 32; o0 += C) {
@@ -507,20 +527,23 @@ __device__ __forceinline__ void put_ring_value(const Work& wk, const __nv_bfloat
 
 // ---------------------------------------------------------------- the kernel
 
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_constant__ Params p,
-                                                                   const __grid_constant__ Args a, unsigned* status) {
+                                                                   const __grid_constant__ Args a, int shared_by, unsigned* status) {
+    const int ctas = SPLIT ? shared_by : 1;
     extern __shared__ unsigned char raw_smem[];
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw_smem) + 127) & ~uintptr_t(127));
     // (the same in every lane, which the compiler knows after the exchange: operands of the products stay uniform)
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) / 32, 0), lane = threadIdx.x % 32;
-    Work wk;
+    Work<SPLIT> wk;
     wk.b = blockIdx.z;
     wk.h = blockIdx.y;
     Seq sq;
     if (!sequence(a, wk.b, sq)) return;
     const int g = p.g, QT = kRows / g;                    // queries of a block
-    const int i0 = int(gridDim.x - 1 - blockIdx.x) * 2 * QT;   // the last queries see the most: first
+    wk.rank = SPLIT ? blockIdx.x % ctas : 0;
+    wk.ctas = ctas;
+    const int i0 = int((gridDim.x - 1 - blockIdx.x) / ctas) * 2 * QT;   // the last queries see the most: first
     if (i0 >= sq.n) return;
     const int nq = min(2 * QT, sq.n - i0);
     const bool two = nq > QT;
@@ -532,7 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
     // an empty sequence (decode) has no position at all
     wk.n_sink = (min(a.sinks, min(wk.lo, wk.p_max + 1)) + kTile - 1) / kTile;
     wk.first = max(wk.n_sink, wk.lo / kTile);
-    wk.n_tile = wk.n_sink + max(0, (wk.p_max + kTile) / kTile - wk.first);
+    const int all_tiles = wk.n_sink + max(0, (wk.p_max + kTile) / kTile - wk.first);
+    wk.n_tile = all_tiles > wk.rank ? (all_tiles - wk.rank + ctas - 1) / ctas : 0;
     const int kn = a.kpc ? 2 : 32 / p.kb, vn = 32 / p.vb; // order of the key's channels (2: as they are) and of positions
 
     // ---- set up ----
@@ -729,32 +753,96 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
             const int qi = m * QT + q_in;
             const bool mine = r < QT * g && qi < nq;
             const size_t row = (sq.row + i0 + qi) * p.hq + wk.h * g + r % g;
-            const float inv = !ok ? NAN : l > 0.f ? 1.f / l : 0.f;
+            if (SPLIT) {
+                // To this CTA's part of the join, over the operands: every product of both blocks is done by then.
+                if (ok && wk.n_tile > 0 && two) ok = wait(&sm.olast[1 - m], 0);
+                float* part = reinterpret_cast<float*>(sm.q[0]) + (m * kRows + r) * kPartPitch<D>;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = 0;
-                if (wk.n_tile > 0) {
-                    tmem_ld32(to + c * 32, o);
-                    tc_wait_ld();
+                    for (int i = 0; i < 32; ++i) o[i] = 0;
+                    if (wk.n_tile > 0) {
+                        tmem_ld32(to + c * 32, o);
+                        tmem_loaded(o);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        reinterpret_cast<uint4*>(part + c * 32)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
-                if (mine) {
-                    uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + c * 32);
+                part[D] = ref;
+                part[D + 1] = ok ? l : NAN;
+            } else {
+                const float inv = !ok ? NAN : l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t w[4];
+                    for (int i = 0; i < 32; ++i) o[i] = 0;
+                    if (wk.n_tile > 0) {
+                        tmem_ld32(to + c * 32, o);
+                        tmem_loaded(o);
+                    }
+                    if (mine) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + c * 32);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[8 * i + 2 * e]) * inv,
-                                                                           __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-                            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[8 * i + 2 * e]) * inv,
+                                                                               __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+                                w[e] = *reinterpret_cast<const uint32_t*>(&h);
+                            }
+                            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
-                        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
+                if (mine && a.lse) a.lse[row] = !ok ? NAN : l > 0.f ? (ref + log2f(l)) * 0.693147180559945309f : -INFINITY;
             }
-            if (mine && a.lse) a.lse[row] = !ok ? NAN : l > 0.f ? (ref + log2f(l)) * 0.693147180559945309f : -INFINITY;
+        }
+        if (SPLIT) {   // a warp a row, D/32 channels a lane; the rows are dealt to the CTAs
+            cluster_sync();
+            namespace cg = cooperative_groups;
+            const cg::cluster_group cl = cg::this_cluster();
+            constexpr int C = D / 32;
+#pragma unroll 1
+            for (int k = wk.rank + ctas * warp; k < 2 * kRows; k += ctas * 8) {
+                const int mm = k / kRows, rr = k % kRows, qi = mm * QT + rr / g;
+                if (rr >= QT * g || qi >= nq) continue;
+                float ref[8], sum[8], v[8][C];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float* part = cl.map_shared_rank(reinterpret_cast<float*>(sm.q[0]), i < ctas ? i : 0) + k * kPartPitch<D>;
+                    ref[i] = i < ctas ? part[D] : kRefNone;
+                    sum[i] = i < ctas ? part[D + 1] : 0.f;
+#pragma unroll
+                    for (int c = 0; c < C; c += 2) {
+                        const float2 x = *reinterpret_cast<const float2*>(part + lane * C + c);
+                        v[i][c] = i < ctas ? x.x : 0.f;
+                        v[i][c + 1] = i < ctas ? x.y : 0.f;
+                    }
+                }
+                float top = ref[0], l = 0.f, o[C];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) top = fmaxf(top, ref[i]);
+#pragma unroll
+                for (int c = 0; c < C; ++c) o[c] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float f = ex2(ref[i] - top);
+                    l = fmaf(sum[i], f, l);
+#pragma unroll
+                    for (int c = 0; c < C; ++c) o[c] = fmaf(v[i][c], f, o[c]);
+                }
+                const float inv = l != 0.f ? 1.f / l : 0.f;   // (NaN stays)
+                const size_t row = (sq.row + i0 + qi) * p.hq + wk.h * g + rr % g;
+#pragma unroll
+                for (int c = 0; c < C; c += 2)
+                    *reinterpret_cast<__nv_bfloat162*>(a.out + row * D + lane * C + c) = __floats2bfloat162_rn(o[c] * inv, o[c + 1] * inv);
+                if (a.lse && lane == 0) a.lse[row] = l != 0.f ? (top + log2f(l)) * 0.693147180559945309f : -INFINITY;
+            }
+            cluster_sync();                               // no CTA leaves while another reads its part
         }
     } else if (warp < 20) {
         // ------------------------------------------------ keys (warps 8-11), values (12-19)
@@ -983,6 +1071,11 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
             }
         }
     }
+    if (SPLIT && warp >= 8) {
+        __syncwarp();
+        cluster_sync();
+        cluster_sync();
+    }
     // every product has been waited for by the weights' warps, or the waits have given up
     tc_fence_before();
     __syncthreads();
@@ -990,26 +1083,44 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
 }
 
 template <int D>
-cudaError_t launch_d(const Params& p, const Args& a, unsigned* status, cudaStream_t s) {
+cudaError_t launch_d(const Params& p, const Args& a, int sms, unsigned* status, cudaStream_t s) {
     static bool opted[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     constexpr int kBytes = int(sizeof(Smem<D>)) + 128;
     if (!opted[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(sink_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
-        if (e != cudaSuccess) return e;
+        for (auto* kernel : {sink_prefill_kernel<D, false>, sink_prefill_kernel<D, true>}) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+            if (e != cudaSuccess) return e;
+        }
         opted[dev] = true;
     }
-    const int per = 2 * (kRows / p.g);
-    const dim3 grid((a.max_q - 1) / per + 1, p.hkv, p.batch);
-    sink_prefill_kernel<D><<<grid, kThreads, kBytes, s>>>(p, a, status);
-    return cudaGetLastError();
+    static_assert(2 * kRows * kPartPitch<D> * 4 <= int(offsetof(Smem<D>, vscale)), "a join's part lies over the operands");
+    const int per = 2 * (kRows / p.g), blocks = (a.max_q - 1) / per + 1;
+    // CTAs that share the tiles of a block of rows: as many as there are SMs for, with four tiles each at least
+    const long long cached = std::min<long long>((long long)p.max_pages * kPage + ring_slots(p, a.kpc), a.len_cap);
+    const long long tiles = std::min(cached, (long long)a.sinks + a.span + per + 2 * kPage) / kTile;
+    const long long all = (long long)blocks * p.hkv * p.batch;
+    int ctas = 1;
+    while (ctas < 8 && all * ctas * 2 <= sms && tiles >= 4 * ctas * 2) ctas *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks * ctas, p.hkv, p.batch);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ctas;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = ctas > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, ctas > 1 ? sink_prefill_kernel<D, true> : sink_prefill_kernel<D, false>, p, a, ctas, status);
 }
 
 }  // namespace
 
-cudaError_t launch_prefill(const Params& p, const Args& a, unsigned* status, cudaStream_t s) {
-    return p.d == 128 ? launch_d<128>(p, a, status, s) : launch_d<64>(p, a, status, s);
+cudaError_t launch_prefill(const Params& p, const Args& a, int sms, unsigned* status, cudaStream_t s) {
+    return p.d == 128 ? launch_d<128>(p, a, sms, status, s) : launch_d<64>(p, a, sms, status, s);
 }
 
 }  // namespace sink
