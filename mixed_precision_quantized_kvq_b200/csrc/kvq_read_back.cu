@@ -12,7 +12,11 @@
 // row: its stores are 16 bytes wide and a warp's are contiguous.  Code rows
 // along channels (keys) give a thread its eight codes in one load; code runs
 // along positions (values, keys with groups along positions) are read as one
-// word of eight channels each, for D/16 neighbouring positions.
+// word of eight channels each, for D/16 neighbouring positions.  Measured on a
+// B200: 88 us for 4096 rows of 16 sequences and 8 heads in bf16 (336 MB, 3.8
+// TB/s); the issue slots of the reconstruction (about 70 for a warp's 256
+// channels) are what is left above the bytes.  Keys and values of a page in one
+// CTA took 96.
 #include "kvq_sink.cuh"
 
 namespace kvq {

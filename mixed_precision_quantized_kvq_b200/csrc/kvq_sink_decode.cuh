@@ -12,18 +12,24 @@
 //
 // What bounds it: the codes and metadata of the visible positions in (116
 // bytes per position and kv-head for 4-bit keys and 2-bit values), and about
-// 900 issue slots a warp for 64 of them, which at this many bytes is the
+// 1100 issue slots a warp for 64 of them, which at this many bytes is the
 // larger part.  Hence the products on mma.sync.m16n8k16 with the positions
 // (scores) or channels (values) as its 16 rows and the up to 8 query heads of
 // a kv-head as its 8 columns: fragments are registers, the codes never go
-// through shared memory a second time.
+// through shared memory a second time.  Measured on a B200: 28.8 us for 16
+// sequences of 32 query and 8 kv-heads over 4096 positions (67.6 MB, 10.3 us at
+// the copy rate), of which about 9 are start-up (dependent loads of length,
+// page table and codes, first fetch of the instructions, the join); 9.3 MB more
+// cost 2.5 us, 56% of the copy rate.
 //
 // Work split: one cluster of 1 to 16 CTAs per (sequence, kv-head); its warps
 // take the 64-position pages in turn (warp w of W: pages w, w + W, ...), then
 // 16-slot pieces of the bf16 ring, each with its own buffers for keys and
-// values filled by cp.async.  The warps' partial sums meet in
-// shared memory, across the cluster through distributed shared memory: no
-// workspace, no atomics, the same result on every run.
+// values filled by cp.async (one stage each: with two stages of both, 12 warps
+// fit an SM instead of 16 and 64 ragged sequences took 69 us instead of 48).
+// The warps' partial sums meet in shared memory, across the cluster through
+// distributed shared memory: no workspace, no atomics, the same result on every
+// run.
 //
 // Fragment layouts (lane = 4*r + c): A rows r and r+8, B column r, D columns
 // 2c and 2c+1.  A tile's scores come out as (position r, heads 2c, 2c+1);
@@ -47,7 +53,7 @@ namespace sink {
 
 using namespace ptx;
 
-constexpr int kMaxWarps = 16;          // what the registers of an SM hold, in one CTA or several
+constexpr int kMaxWarps = 16;        // what the registers of an SM hold, in one CTA or several
 constexpr int kHeads = 8;            // columns of the products
 constexpr int kRing = 16;            // ring slots per piece
 constexpr float kRefNone = -1e30f;   // reference exponent before any position
@@ -829,7 +835,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) sink_decode_kernel(const __gri
 
 // ---------------------------------------------------------------- launch
 
-// CTAs per (sequence, kv-head).  A CTA of a round costs about its items (pages or ring pieces, shared by its warps)
+// CTAs per (sequence, kv-head), at most 16: one sequence of 131072 positions at 8 bits takes 101 us with 16, 144 with 8.
+// A CTA of a round costs about its items (pages or ring pieces, shared by its warps)
 // plus one and a half for its start and its end; the rounds are what `slots` CTAs at a time make of all of them.
 inline int split_ctas(long long pairs, int items, int warps, int slots, int most) {
     int best = 1;
