@@ -838,6 +838,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) sink_decode_kernel(const __gri
 // CTAs per (sequence, kv-head), at most 16: one sequence of 131072 positions at 8 bits takes 101 us with 16, 144 with 8.
 // A CTA of a round costs about its items (pages or ring pieces, shared by its warps)
 // plus one and a half for its start and its end; the rounds are what `slots` CTAs at a time make of all of them.
+// (64 ragged sequences of 8 kv-heads: 48 us with the 512 CTAs that this gives, 63 with 1536, 100 with 4096; CTAs of two
+// warps, which would fill the SMs more evenly, took 56.)
 inline int split_ctas(long long pairs, int items, int warps, int slots, int most) {
     int best = 1;
     double least = 1e30;

@@ -9,9 +9,9 @@
 // query row; O / l is rounded to bf16.  Bound by the tensor cores and the
 // exponentials (one per visible pair: 16 a clock and SM, which takes as long as
 // the two products at head_dim 128), in practice by the issue slots and the
-// hand-overs of a tile.  Measured on a B200: 752 us for chunks of 512 queries of
-// 16 sequences at 4096 positions, 32 query and 8 kv-heads (550 GFLOP: 731
-// TFLOP/s, 44% of a library product's rate); a tile takes 2.4 us a CTA of which
+// hand-overs of a tile.  Measured on a B200: 738 us for chunks of 512 queries of
+// 16 sequences at 4096 positions, 32 query and 8 kv-heads (550 GFLOP: 745
+// TFLOP/s, 45% of a library product's rate); a tile takes 2.4 us a CTA of which
 // the tensor core works 0.7, a CTA's start and end about 15.
 //
 // One CTA per SM takes 256 rows of one (sequence, kv-head): two blocks of 128,
@@ -366,8 +366,9 @@ __device__ __forceinline__ void put_key_of(int kg, const uint4 (&raw)[4], const 
 }
 
 // Keys with groups along positions: codes of channels 2*cp (raw[0..1]) and 2*cp + 1 (raw[2..3]) at half the positions of a
-// page, 32 from t0 on, to rows of the key tile.
-template <int BITS, int D>
+// page, 32 from t0 on, to rows of the key tile.  ALL: every one of them lives in the page (a check at each store instead:
+// 564 us against 282 for two prompts of 3000 positions).
+template <int BITS, int D, bool ALL>
 __device__ __forceinline__ void put_key_pairs(const uint4 (&raw)[4], const uint32_t* meta, int kshift, int t0, int valid, int vn,
                                               unsigned char* to) {
     constexpr int N = 32 / BITS, W = 32 / N;             // codes a word, words a channel
@@ -395,9 +396,18 @@ __device__ __forceinline__ void put_key_pairs(const uint4 (&raw)[4], const uint3
 #pragma unroll
             for (int b = 0; b < 5; ++b)
                 if (t & (1 << b)) off += step[b];
-            if (t0 + t < valid) *reinterpret_cast<uint32_t*>(to + off) = bits(k);
+            if (ALL || t0 + t < valid) *reinterpret_cast<uint32_t*>(to + off) = bits(k);
         }
     }
+}
+
+template <int BITS, int D>
+__device__ __forceinline__ void put_key_pairs_of(const uint4 (&raw)[4], const uint32_t* meta, int kshift, int t0, int valid, int vn,
+                                                 unsigned char* to) {
+    if (t0 + 32 <= valid)
+        put_key_pairs<BITS, D, true>(raw, meta, kshift, t0, valid, vn, to);
+    else
+        put_key_pairs<BITS, D, false>(raw, meta, kshift, t0, valid, vn, to);
 }
 
 // half a ring row to its row of the key tile, in the channel order of words of N codes
@@ -534,7 +544,9 @@ __device__ __forceinline__ void put_ring_value(const Work<SPLIT>& wk, const __nv
 
 // ---------------------------------------------------------------- the kernel
 
-template <int D, bool SPLIT>
+// KPC: keys with groups along positions (with both forms of the keys in one build, chunks of 512 at 4096 positions took 752
+// to 780 us against 738, as the compiler laid out the loop of the keys).
+template <int D, bool SPLIT, bool KPC>
 __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_constant__ Params p,
                                                                    const __grid_constant__ Args a, int shared_by, unsigned* status) {
     const int ctas = SPLIT ? shared_by : 1;
@@ -555,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
     const int nq = min(2 * QT, sq.n - i0);
     const bool two = nq > QT;
     wk.L = sq.L;
-    wk.Lq = paged_len(p, a.kpc, sq.L);
+    wk.Lq = paged_len(p, KPC, sq.L);
     wk.p_max = sq.base + i0 + nq - 1;
     wk.lo = span_begin(sq.base + i0, a.span);
     wk.sinks = a.sinks;
@@ -564,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
     wk.first = max(wk.n_sink, wk.lo / kTile);
     const int all_tiles = wk.n_sink + max(0, (wk.p_max + kTile) / kTile - wk.first);
     wk.n_tile = all_tiles > wk.rank ? (all_tiles - wk.rank + ctas - 1) / ctas : 0;
-    const int kn = a.kpc ? 2 : 32 / p.kb, vn = 32 / p.vb; // order of the key's channels (2: as they are) and of positions
+    const int kn = KPC ? 2 : 32 / p.kb, vn = 32 / p.vb; // order of the key's channels (2: as they are) and of positions
 
     // ---- set up ----
     if (threadIdx.x == 0) {
@@ -853,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
         }
     } else if (warp < 20) {
         // ------------------------------------------------ keys (warps 8-11), values (12-19)
-        const int R = ring_slots(p, a.kpc);
+        const int R = ring_slots(p, KPC);
         // table entry of tile j's page (-1 past what any row sees); looked at a tile later, so nothing waits for it
         auto page_of = [&](int j) -> int {
             if (j >= wk.n_tile) return -1;
@@ -871,17 +883,17 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
             uint4 raw[4];
             uint32_t meta[4];
             // this thread's codes and metadata in page 0, and what lies between pages
-            const int part = a.kpc ? run_bytes / 2 : p.krow_bytes / 2, groups = min(4, max(1, D / 2 >> kshift));
+            const int part = KPC ? run_bytes / 2 : p.krow_bytes / 2, groups = min(4, max(1, D / 2 >> kshift));
             const size_t code_step = size_t(p.hkv) * kPage * p.krow_bytes, meta_step = size_t(p.hkv) * kPage * p.nkg;
             const uint8_t* codes = p.k_codes + size_t(wk.h) * kPage * p.krow_bytes +
-                                   (a.kpc ? 2 * slot * ch + part_offset(half * part, ch, D * 16)
+                                   (KPC ? 2 * slot * ch + part_offset(half * part, ch, D * 16)
                                           : slot * p.kch + part_offset(half * part, p.kch, kPage * 16));
             // (tokens: groups from that of channel half * D/2 on: D/2 / kg of them, or the one that holds them all)
             const uint32_t* metas = p.k_meta + (size_t(wk.h) * kPage + slot) * p.nkg + (half * (D / 2) >> kshift);
             auto load = [&]() {
                 if (pg < 0) return;
                 const uint8_t* at = codes + pg * code_step;
-                if (a.kpc) {
+                if (KPC) {
                     if (slot >= D / 2) return;
                     uint4 x[2], y[2];
                     load_part<2>(x, at, D * 16, part);
@@ -906,14 +918,14 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                 if (!ok) break;
                 unsigned char* sk = sm.k[st];
                 unsigned char* row = sk + slot_of(slot, vn) * 16 + half * (D / 16) * kKeyPitch;
-                if (a.kpc) {
+                if (KPC) {
                     if (slot < D / 2 && pg >= 0) {
                         const uint32_t* m = p.k_meta + (size_t(pg) * p.hkv + wk.h) * size_t(kPage >> kshift) * D + 2 * slot;
                         unsigned char* col = sk + (slot >> 2) * kKeyPitch + (slot & 3) * 4 + half * (32 * 16);
-                        if (p.kb == 4) put_key_pairs<4, D>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
-                        if (p.kb == 8) put_key_pairs<8, D>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
-                        if (p.kb == 2) put_key_pairs<2, D>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
-                        if (p.kb == 1) put_key_pairs<1, D>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
+                        if (p.kb == 4) put_key_pairs_of<4, D>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
+                        if (p.kb == 8) put_key_pairs_of<8, D>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
+                        if (p.kb == 2) put_key_pairs_of<2, D>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
+                        if (p.kb == 1) put_key_pairs_of<1, D>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
                     }
                 } else if (pg >= 0 && x < wk.Lq) {
                     if (p.kb == 4) put_key_of<4, D>(p.kg, raw, meta, row);
@@ -1096,7 +1108,8 @@ cudaError_t launch_d(const Params& p, const Args& a, int sms, unsigned* status, 
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     constexpr int kBytes = int(sizeof(Smem<D>)) + 128;
     if (!opted[dev]) {
-        for (auto* kernel : {sink_prefill_kernel<D, false>, sink_prefill_kernel<D, true>}) {
+        for (auto* kernel : {sink_prefill_kernel<D, false, false>, sink_prefill_kernel<D, true, false>,
+                             sink_prefill_kernel<D, false, true>, sink_prefill_kernel<D, true, true>}) {
             const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
             if (e != cudaSuccess) return e;
         }
@@ -1121,7 +1134,9 @@ cudaError_t launch_d(const Params& p, const Args& a, int sms, unsigned* status, 
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = ctas > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, ctas > 1 ? sink_prefill_kernel<D, true> : sink_prefill_kernel<D, false>, p, a, ctas, status);
+    auto* kernel = a.kpc ? ctas > 1 ? sink_prefill_kernel<D, true, true> : sink_prefill_kernel<D, false, true>
+                   : ctas > 1 ? sink_prefill_kernel<D, true, false> : sink_prefill_kernel<D, false, false>;
+    return cudaLaunchKernelEx(&cfg, kernel, p, a, ctas, status);
 }
 
 }  // namespace
