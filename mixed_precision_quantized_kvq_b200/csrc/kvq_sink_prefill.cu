@@ -637,9 +637,11 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
             const uint32_t to = tmem + 256 + m * D + lanes;
             const int q_in = r / g;
             // ---- queries, while the first tiles come in ----
+            // (A CTA of a cluster that has no tile has no use for them.  Its warps wait for no product, and so not for each
+            // other, before they write their part of the join over the queries' place: nothing else may be written there.)
             const float scale = fabsf(a.scale_log2), sign = a.scale_log2 < 0.f ? -1.f : 1.f;
             float factor = 0.f;
-            {
+            if (!SPLIT || wk.n_tile > 0) {
                 constexpr int kPer = 32 / (D / 8);        // rows of the warp at a time, D/8 lanes each
                 const int oct = lane % (D / 8), sub = lane / (D / 8), first = r - lane;
                 // each lane knows its own row's place (-1: no such row)
@@ -773,7 +775,9 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
             const bool mine = r < QT * g && qi < nq;
             const size_t row = (sq.row + i0 + qi) * p.hq + wk.h * g + r % g;
             if (SPLIT) {
-                // To this CTA's part of the join, over the operands: every product of both blocks is done by then.
+                // To this CTA's part of the join, over the operands.  With tiles, every product of both blocks is done by
+                // then, and a block's products come after all of its queries and of the tiles that the other warps wrote;
+                // without, neither queries nor tiles are written.
                 if (ok && wk.n_tile > 0 && two) ok = wait(&sm.olast[1 - m], 0);
                 float* part = reinterpret_cast<float*>(sm.q[0]) + (m * kRows + r) * kPartPitch<D>;
 #pragma unroll 1
