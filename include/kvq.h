@@ -369,12 +369,16 @@ int kvq_dequantize(const kvq_layout* layout, const kvq_cache* cache,
  *    once.  Single tokens over key groups of 32 channels or more multiply the
  *    codes themselves: out is within 1e-3 + 1e-3*|o| (+ its rounding) and lse
  *    within 1e-3 + 1e-3*|lse| of the same sums in fp64.  Chunks, and single
- *    tokens of the other layouts, round keys, values and weights to fp16 (and
- *    queries that are fp32 or rotated), each by up to 2^-11 of itself: a score
- *    is off by at most D = 2^-11 sum_j |q_j k_j| * |sm_scale| (twice that with
- *    the query's rounding), lse by D, out by a factor within exp(+-2D) of each
- *    weight and 2^-10 of sum a |v|.  There reconstructed keys and values must
- *    lie within +-65504.
+ *    tokens of the other layouts, round keys and values to fp16 (and queries
+ *    that are fp32 or rotated), each by up to 2^-11 of itself or 2^-25, the
+ *    larger: a score is off by at most
+ *        D = |sm_scale| sum_j |q_j| (2^-11 |k_j| + 2^-25)
+ *    (2^-10 with the query's rounding) and lse by D.  Weights are rounded to
+ *    fp16 too, by up to 2^-11 of themselves or 2^-33 of the largest: out is
+ *    off by a factor within exp(+-2D) of each weight, by 2^-10 sum a |v| +
+ *    2^-25 and by 2^-33 a_max sum |v| over the visible positions.  There
+ *    reconstructed keys and values must lie within +-65504: a value beyond, or
+ *    NaN, reaches its channel of the chunk's other queries.
  *  - No workspace; calls on different streams may overlap as long as no
  *    call writes the cache.  Results do not depend on what else runs. */
 

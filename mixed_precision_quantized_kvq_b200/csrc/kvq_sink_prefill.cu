@@ -23,7 +23,7 @@
 // tile a block took 0.91 ms at the size above).  Warps:
 //   0-3, 4-7   weights of block 0 and 1: thread = row.  S from tensor memory
 //              once, P back over S as fp16; reference and O are adjusted only
-//              when a score exceeds the reference by more than 14 binades.
+//              when a score exceeds the reference by more than 15 binades.
 //   8-11       reconstruct keys: thread = half the channels of a position
 //              (groups along positions: two channels of half the positions).
 //   12-19      values: thread = half the positions of a channel.  Codes and
@@ -68,6 +68,7 @@ constexpr int kKeyThreads = 128, kValueThreads = 256;
 constexpr int kStages = 4;
 constexpr uint64_t kLimitNs = 2000000000ull;  // a wait that takes longer gives up
 constexpr float kRefNone = -1e30f;
+constexpr float kTopWeight = 15.f, kLowTop = 8.f;   // the largest weight's exponent: at most, and after a rise
 constexpr int kKeyPitch = kTile * 16 + 16;    // bytes between 16-byte columns of the key tile and of the queries: the
 constexpr int kQueryPitch = kRows * 16 + 16;  // extra piece puts neighbouring columns of a row in different banks
 
@@ -728,10 +729,14 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                     for (int i = 1; i < 8; ++i) mx[e] = fmaxf(mx[e], __uint_as_float(s[e >> 2][(e & 3) * 8 + i]));
                 }
                 const float need = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * factor;
-                // Weights are taken against the reference of the tiles before.  Should a score lie more than 2^14 above it (the
-                // first tile's always do), the reference is raised and O brought down to it.
-                if (__builtin_expect(__any_sync(0xffffffffu, need > ref + 14.f), 0)) {
-                    const float up = fmaxf(ref, need), f = ex2(ref - up);
+                // Weights are taken against the reference of the tiles before.  Should one exceed 2^15, the most that fp16
+                // holds (the first tile's always do), the reference is raised and O brought down to it: to 2^8 below the
+                // largest weight, which so lies from 2^8 to 2^15.  A weight then keeps 11 bits down to 2^-22 of the largest and
+                // counts down to 2^-33, and what a sink leaves to many others is not lost.  (Room above for fewer rises
+                // or range below: 16 chunks of 512 at 4096 positions take 756 us with the largest at 2^0, 761 at 2^6,
+                // 765 at 2^8, 769 at 2^10.)
+                if (__builtin_expect(__any_sync(0xffffffffu, need > ref + kTopWeight), 0)) {
+                    const float up = fmaxf(ref, need - kLowTop), f = ex2(ref - up);
                     ref = up;
                     l *= f;
                     if (j > 0) {

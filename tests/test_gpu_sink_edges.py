@@ -1,5 +1,5 @@
-"""The attention with sinks where its parts meet: clusters whose CTAs have no tile, against fp64 numpy over the
-oracle's cache."""
+"""The attention with sinks at its edges, against fp64 numpy over the oracle's cache: clusters whose CTAs have no
+tile, weights far below the largest."""
 import numpy as np
 import pytest
 import torch
@@ -7,8 +7,8 @@ import torch
 import mixed_precision_quantized_kvq_b200 as kvq
 import sink_reference as ref
 import workloads as wl
-from gpu_harness import torch_raw
-from test_gpu_sink import build, check_attention, i32, poison, small
+from gpu_harness import Pair, torch_raw
+from test_gpu_sink import INF, build, check_attention, i32, poison, small
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,50 @@ def test_single_tokens_in_clusters_with_more_ctas_than_tiles(layout):
         out, lse = kvq.sink_decode_attention(pair.glay, pair.gcache, q, pair.glens, 512 * 64, 4, 4096)
         differ += (out != first).sum() + (lse != first_lse).sum()
     assert int(differ) == 0
+
+
+# ---------------------------------------------------------------- weights far below the largest
+
+FAR = {
+    "exact_codes": dict(),
+    "d64": dict(head_dim=64, v_group=64),
+    "groups16": dict(k_group=16, v_group=32),
+    "per_channel": dict(k_per_channel=True),
+}
+
+
+@pytest.mark.parametrize("low,high", [(20, 26), (26, 30)])
+@pytest.mark.parametrize("form", ["token", "chunk shared by a cluster", "chunk"])
+@pytest.mark.parametrize("layout", list(FAR))
+def test_one_page_far_above_the_others(layout, form, low, high):
+    """A first page of weight 1 and value 0, and 30000 positions 2^-low to 2^-high below it with values around 1: what
+    they add up to is the whole output.  Keys are constant over their groups, values over a position, and queries have
+    one channel, so scores, keys and values are exact and the weights' rounding to fp16 is all that counts.  With the
+    largest weight at 2^8 or more, each is off by at most 2^-11 of itself or half a subnormal step, 2^-25:
+        |out error| <= 2^-11 sum a |v| + 2^-33 a_max sum |v|
+    and the fp32 sums add to the former: about 500 tiles' sums of the weights and 4 products a tile, each off by at most
+    2^-23 of the whole: 2^-14 + 2^-12."""
+    w = small(batch=1, num_kv_heads=1, num_q_heads=2, **FAR[layout])
+    L, d, r = 30016, w.head_dim, np.random.default_rng(5)
+    key = np.repeat(-r.integers(low * 8, high * 8, L // 64) / 8.0, 64)   # constant over a page: 1/8 is a bf16 step there
+    val = r.integers(32, 97, L) / 64.0
+    key[:64], val[:64] = 0.0, 0.0
+    pair = Pair(w, np.array([L], np.int32))
+    pair.lens[:] = 0
+    pair.glens.zero_()
+    rows = lambda x: wl.bf16_bits(np.repeat(x.astype(np.float32), d).reshape(L, 1, d))  # noqa: E731
+    pair.append(rows(key), rows(val), np.array([0, L]))
+    pair.compare_cache()
+    n = np.array([1 if form == "token" else 40])
+    q = np.zeros((int(n[0]), 2, d), np.float32)
+    q[:, :, 3] = 1.0
+    raw, scale, cu = torch_raw(wl.bf16_bits(q)), float(np.log(2.0)), i32([0, n[0]])
+    if form == "token":
+        out, lse = kvq.sink_decode_attention(pair.glay, pair.gcache, raw, pair.glens, L, 64, INF, scale)
+    else:                                        # (a bound of 20000 queries: blocks enough for every SM)
+        out, lse = kvq.sink_prefill_attention(pair.glay, pair.gcache, raw, cu, pair.glens, 40 if "cluster" in form else 20000,
+                                              64, INF, scale)
+    want, want_lse = ref.attention(pair.ocache, pair.pt, None, q.astype(np.float64), n, pair.lens, 64, INF, scale)
+    tol = (2.0 ** -11 + 2.0 ** -12 + 2.0 ** -14) * want + 2.0 ** -33 * np.exp(-want_lse)[:, :, None] * val.sum()
+    ref.check_bf16(out.float().cpu().numpy(), want, tol=tol)
+    ref.check_lse(lse.cpu().numpy(), want_lse, np.full(want_lse.shape, 2.0 ** -14))
