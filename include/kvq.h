@@ -357,7 +357,8 @@ int kvq_dequantize(const kvq_layout* layout, const kvq_cache* cache,
  *    (its entry set to -1, the page reused) once all its positions are >=
  *    sinks and more than span - 1 behind every query still to come.
  *  - sinks, span >= 0; span = INT_MAX sees every position, span = 0 only
- *    the sinks.  A query that sees nothing gets out = 0, lse = -inf.
+ *    the sinks.  A query that sees nothing gets out = 0, lse = -inf; one
+ *    whose scores hold a NaN gets NaN for both.
  *  - Every layout that the library accepts; `span` is independent of
  *    layout->window (what the bf16 ring holds).
  *  - q is KVQ_BF16 or KVQ_F32, its rows [Hq][d] start q_stride elements

@@ -784,11 +784,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32) sink_decode_kernel(const __gri
         if (ctas > 1) {
             reinterpret_cast<float2*>(parts(0))[e] = o;
         } else {
-            const float l = hd.qsum[x][0], inv = l > 0.f ? 1.f / l : 0.f;
+            const float l = hd.qsum[x][0], inv = l != 0.f ? 1.f / l : 0.f;   // (NaN stays)
             const size_t row = size_t(b) * p.hq + h * p.g + x;
             reinterpret_cast<__nv_bfloat162*>(a.out + row * D)[e % (D / 2)] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
             if (a.lse && e % (D / 2) == 0)
-                a.lse[row] = l > 0.f ? (hd.factor[x] + log2f(l)) * 0.693147180559945309f : -INFINITY;
+                a.lse[row] = l != 0.f ? (hd.factor[x] + log2f(l)) * 0.693147180559945309f : -INFINITY;
         }
     }
     if (ctas == 1) return;
@@ -825,10 +825,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32) sink_decode_kernel(const __gri
                 o.y = fmaf(v[i].y, f, o.y);
             }
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l != 0.f ? 1.f / l : 0.f;
         const size_t row = size_t(b) * p.hq + h * p.g + x;
         reinterpret_cast<__nv_bfloat162*>(a.out + row * D)[e % (D / 2)] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-        if (a.lse && e % (D / 2) == 0) a.lse[row] = l > 0.f ? (top + log2f(l)) * 0.693147180559945309f : -INFINITY;
+        if (a.lse && e % (D / 2) == 0) a.lse[row] = l != 0.f ? (top + log2f(l)) * 0.693147180559945309f : -INFINITY;
     }
     cl.sync();                                           // no CTA leaves while another reads its part
 }

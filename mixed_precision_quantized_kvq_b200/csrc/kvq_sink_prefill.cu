@@ -801,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                 part[D] = ref;
                 part[D + 1] = ok ? l : NAN;
             } else {
-                const float inv = !ok ? NAN : l > 0.f ? 1.f / l : 0.f;
+                const float inv = !ok ? NAN : l != 0.f ? 1.f / l : 0.f;   // (NaN stays)
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
@@ -826,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                         }
                     }
                 }
-                if (mine && a.lse) a.lse[row] = !ok ? NAN : l > 0.f ? (ref + log2f(l)) * 0.693147180559945309f : -INFINITY;
+                if (mine && a.lse) a.lse[row] = !ok ? NAN : l != 0.f ? (ref + log2f(l)) * 0.693147180559945309f : -INFINITY;
             }
         }
         if (SPLIT) {   // a warp a row, D/32 channels a lane; the rows are dealt to the CTAs

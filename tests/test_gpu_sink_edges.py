@@ -1,5 +1,5 @@
 """The attention with sinks at its edges, against fp64 numpy over the oracle's cache: clusters whose CTAs have no
-tile, weights far below the largest."""
+tile, weights far below the largest, queries with NaN."""
 import numpy as np
 import pytest
 import torch
@@ -127,3 +127,34 @@ def test_one_page_far_above_the_others(layout, form, low, high):
     tol = (2.0 ** -11 + 2.0 ** -12 + 2.0 ** -14) * want + 2.0 ** -33 * np.exp(-want_lse)[:, :, None] * val.sum()
     ref.check_bf16(out.float().cpu().numpy(), want, tol=tol)
     ref.check_lse(lse.cpu().numpy(), want_lse, np.full(want_lse.shape, 2.0 ** -14))
+
+
+# ---------------------------------------------------------------- NaN
+
+@pytest.mark.parametrize("form", ["token", "chunk shared by a cluster", "chunk"])
+@pytest.mark.parametrize("layout", list(JOINED))
+def test_a_query_with_nan(layout, form):
+    """Its outputs and lse are NaN in every form (an lse of -inf would say that it saw nothing); the other heads and rows
+    keep their bits; a query that sees nothing has 0 and -inf whatever it holds."""
+    w = small(batch=2, num_kv_heads=2, num_q_heads=6, **JOINED[layout])
+    pair = build(w, [700, 90])
+    n = np.array([1, 1] if form == "token" else [60, 33])
+    raw, _ = ref.queries(w, int(n.sum()))
+    q, cu = torch_raw(raw), i32(np.concatenate([[0], np.cumsum(n)]))
+
+    def call(span):
+        if form == "token":
+            return kvq.sink_decode_attention(pair.glay, pair.gcache, q, pair.glens, 700, 4 if span else 0, span)
+        bound = 60 if "cluster" in form else 20000
+        return kvq.sink_prefill_attention(pair.glay, pair.gcache, q, cu, pair.glens, bound, 4 if span else 0, span)
+
+    out, lse = (t.clone() for t in call(600))
+    bad = torch.zeros_like(lse, dtype=torch.bool)
+    for row, head, channel in ((0, 1, 5), (0, 3, 0), (int(n.sum()) - 1, 5, w.head_dim - 1)):
+        q[row, head, channel] = float("nan")
+        bad[row, head] = True
+    got, got_lse = call(600)
+    assert torch.all(got[bad].isnan()) and torch.all(got_lse[bad].isnan())
+    assert torch.equal(got[~bad], out[~bad]) and torch.equal(got_lse[~bad], lse[~bad])
+    got, got_lse = call(0)
+    assert torch.all(got == 0) and torch.all(got_lse == -float("inf"))
