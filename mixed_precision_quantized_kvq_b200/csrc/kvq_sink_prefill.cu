@@ -1034,7 +1034,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                     if (p.vb == 4) put_value<4, D>(vs, vz, raw, to);
                     if (p.vb == 8) put_value<8, D>(vs, vz, raw, to);
                     if (p.vb == 1) put_value<1, D>(vs, vz, raw, to);
-                    if (y0 + 32 > wk.Lq) {                // ring positions (the page's codes gave zeros there)
+                    if (y0 + 32 > wk.Lq && wk.Lq < wk.L) {   // ring positions (the page's codes gave zeros there)
                         const __nv_bfloat16* win = p.v_win + (size_t(wk.b) * p.hkv + wk.h) * R * D + ch;
                         if (p.vb == 2) put_ring_value<16, D>(wk, win, R, y0, to);
                         if (p.vb == 4) put_ring_value<8, D>(wk, win, R, y0, to);
