@@ -4,6 +4,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "kvq_internal.cuh"
@@ -16,13 +17,13 @@ namespace {
 using kvq::Params;
 
 constexpr int kMaxDevices = 64;
-int g_sm_count[kMaxDevices];   // 0 = not queried yet
+std::atomic<int> g_sm_count[kMaxDevices];   // 0 = not queried yet (host threads may ask side by side)
 
 int device_sm_count() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 148;
-    if (dev < kMaxDevices && g_sm_count[dev] > 0) return g_sm_count[dev];
-    int n = 0;
+    int n = dev < kMaxDevices ? g_sm_count[dev].load() : 0;
+    if (n > 0) return n;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
         cudaGetLastError();
         n = 148;

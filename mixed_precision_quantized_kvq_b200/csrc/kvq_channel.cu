@@ -6,6 +6,8 @@
 // 512 threads, about kg*d*10 bytes of shared memory) reads ring slots of the
 // positions it quantizes; the ring kernel (grid: kv-heads x sequences)
 // then writes the new positions that stay in the window.
+#include <atomic>
+
 #include "kvq_channel.cuh"
 #include "kvq_channel_body.cuh"
 
@@ -88,7 +90,7 @@ cudaError_t launch_append_per_channel(const Params& p, const void* k_new, const 
     v.cu_new = cu_new;
     v.lens = lens;
     // opt in once per device, for the largest size (d 128, groups of 64)
-    static bool configured[64];
+    static std::atomic<bool> configured[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     cudaError_t e;

@@ -4,6 +4,8 @@
 // dispatched here.
 #pragma once
 
+#include <atomic>
+
 #include <cudaTypedefs.h>
 
 #include "kvq_decode_mma.cuh"
@@ -56,7 +58,7 @@ template <int KB, int VB, int NH>
 cudaError_t launch_one(const Params& p, const void* q, int q_bf16, const int32_t* lens, int max_len, float sl2,
                        float* out, float* lse, float* part, uint32_t* tickets, int ctas, int after_append, unsigned* status, cudaStream_t s) {
     auto kern = decode_mma_kernel<KB, VB, NH>;
-    static bool configured[64];
+    static std::atomic<bool> configured[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!configured[dev]) {

@@ -14,6 +14,8 @@
 // bf16 window.
 #include <math.h>
 
+#include <atomic>
+
 #include "kvq_internal.cuh"
 
 namespace kvq {
@@ -427,16 +429,18 @@ __device__ unsigned int g_decode_status[2];
 
 namespace {
 constexpr int kMaxDev = 64;
-unsigned* g_status_addr[kMaxDev];
+std::atomic<unsigned*> g_status_addr[kMaxDev];   // host threads may look it up side by side
 unsigned* status_ptr() {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return nullptr;
-    if (!g_status_addr[dev]) {
+    unsigned* at = g_status_addr[dev];
+    if (!at) {
         void* a = nullptr;
         if (cudaGetSymbolAddress(&a, g_decode_status) != cudaSuccess) return nullptr;
-        g_status_addr[dev] = static_cast<unsigned*>(a);
+        at = static_cast<unsigned*>(a);
+        g_status_addr[dev] = at;
     }
-    return g_status_addr[dev];
+    return at;
 }
 }  // namespace
 

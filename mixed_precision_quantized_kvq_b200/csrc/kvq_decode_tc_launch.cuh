@@ -2,6 +2,8 @@
 // kvq_decode_tc_k{1,2,4,8}.cu with KVQ_TC_KB set to the key bit width.
 #pragma once
 
+#include <atomic>
+
 #include "kvq_decode_tc.cuh"
 
 namespace kvq {
@@ -12,7 +14,7 @@ cudaError_t launch_one(const Params& p, const void* q, int q_bf16, const int32_t
                        float* ws_o, float* ws_ml, const DecodePlan& pl, unsigned* status, cudaStream_t s) {
     using LY = Layout<KB, VB, NHC>;
     auto kern = decode_tc_kernel<KB, VB, NHC>;
-    static bool configured[64];
+    static std::atomic<bool> configured[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;

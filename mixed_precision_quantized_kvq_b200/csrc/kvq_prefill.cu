@@ -5,6 +5,8 @@
 // and about 117 KB (150 KB with key rotation) of dynamic shared memory per
 // CTA at head_dim 128.  CTAs whose query tile lies past their sequence's
 // chunk return at once.
+#include <atomic>
+
 #include "kvq_prefill.cuh"
 #include "kvq_prefill_body.cuh"
 
@@ -41,7 +43,7 @@ __global__ void __launch_bounds__(prefill::kThreads) prefill_attention_kernel(pr
 template <int D>
 cudaError_t launch_d(const prefill::View& v, cudaStream_t s) {
     // opt in once per device, for the largest size (with rotation)
-    static bool configured[64];
+    static std::atomic<bool> configured[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!configured[dev]) {

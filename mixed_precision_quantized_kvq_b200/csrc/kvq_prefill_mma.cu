@@ -23,6 +23,8 @@
 // and values [channel][position] (the B operands' k-contiguous order), in
 // 16-byte chunks swizzled by row so that ldmatrix reads hit 8 distinct bank
 // groups.
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefill_mma_kernel(const prefill:
 
 template <int KB, int VB>
 cudaError_t launch_kv(const prefill::View& v, cudaStream_t s) {
-    static bool configured[64];
+    static std::atomic<bool> configured[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!configured[dev]) {

@@ -42,6 +42,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kvq_sink.cuh"
 #include "kvq_tc_ptx.cuh"
@@ -859,12 +860,13 @@ template <int D, int KB, int VB, bool LO>
 cudaError_t launch_decode_one(const Params& p, const Args& a, int sms, cudaStream_t s) {
     auto* kernel = sink_decode_kernel<D, KB, VB, LO>;
     // per device, once: large shared memory, and the largest cluster that fits at it (16 is beyond what every device
-    // has to offer, 8 is not)
-    static int largest[64];
+    // has to offer, 8 is not); two threads may both find it
+    static std::atomic<int> largest[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     constexpr int kMost = 227 * 1024;
-    if (!largest[dev]) {
+    int most_ctas = largest[dev];
+    if (!most_ctas) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
@@ -883,7 +885,8 @@ cudaError_t launch_decode_one(const Params& p, const Args& a, int sms, cudaStrea
             cudaGetLastError();
             n = 0;
         }
-        largest[dev] = n > 0 ? 16 : 8;
+        most_ctas = n > 0 ? 16 : 8;
+        largest[dev] = most_ctas;
     }
     // four warps a CTA, or as many up to eight as bring the most warps onto an SM (large buffers)
     int warps = 4, per_sm = 1;
@@ -898,7 +901,7 @@ cudaError_t launch_decode_one(const Params& p, const Args& a, int sms, cudaStrea
     const int smem = decode_smem<D, KB, VB>(p, warps);
     const long long bound = std::min<long long>(a.len_cap, (long long)a.sinks + a.span + 2 * kPage);
     const int items = int((bound + kPage - 1) / kPage) + (std::min(p.W, a.len_cap) + kRing - 1) / kRing;
-    const int n = split_ctas((long long)p.batch * p.hkv, items, warps, sms * per_sm, largest[dev]);
+    const int n = split_ctas((long long)p.batch * p.hkv, items, warps, sms * per_sm, most_ctas);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(n, p.hkv, p.batch);
     cfg.blockDim = dim3(32 * warps);

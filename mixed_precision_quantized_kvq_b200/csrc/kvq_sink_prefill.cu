@@ -46,6 +46,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include <cooperative_groups.h>
 #include <stddef.h>
@@ -1112,7 +1113,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
 
 template <int D>
 cudaError_t launch_d(const Params& p, const Args& a, int sms, unsigned* status, cudaStream_t s) {
-    static bool opted[64];
+    static std::atomic<bool> opted[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     constexpr int kBytes = int(sizeof(Smem<D>)) + 128;

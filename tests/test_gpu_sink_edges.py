@@ -1,5 +1,9 @@
 """The attention with sinks at its edges, against fp64 numpy over the oracle's cache: clusters whose CTAs have no
-tile, weights far below the largest, queries with NaN."""
+tile, weights far below the largest, queries with NaN, first calls from several threads."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -158,3 +162,46 @@ def test_a_query_with_nan(layout, form):
     assert torch.equal(got[~bad], out[~bad]) and torch.equal(got_lse[~bad], lse[~bad])
     got, got_lse = call(0)
     assert torch.all(got == 0) and torch.all(got_lse == -float("inf"))
+
+
+# ---------------------------------------------------------------- threads
+
+THREADS = """
+import threading
+import numpy as np, torch
+from test_gpu_sink import build, i32, small
+import mixed_precision_quantized_kvq_b200 as kvq
+import sink_reference as ref
+from gpu_harness import torch_raw
+
+pairs = [build(small(batch=2, **kw), [300, 90]) for kw in (dict(window=16), dict(k_per_channel=True, window=16))]
+q, cu = torch_raw(ref.queries(pairs[0].w, 100)[0]), i32([0, 60, 100])
+start, got, failed = threading.Barrier(8), [None] * 8, []
+
+def work(i):
+    try:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            start.wait()
+            got[i] = [t for p in pairs for t in (
+                *kvq.sink_decode_attention(p.glay, p.gcache, q[:2], p.glens, 300, 4, 100),
+                *kvq.sink_prefill_attention(p.glay, p.gcache, q, cu, p.glens, 60, 4, 100),
+                kvq.prefill_attention(p.glay, p.gcache, q, cu, p.glens, 60)[0])]
+            torch.cuda.current_stream().synchronize()
+    except Exception as e:
+        failed.append(e)
+
+torch.cuda.synchronize()
+threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+assert not failed, failed
+assert all(torch.equal(a, b) for other in got[1:] for a, b in zip(got[0], other))
+"""
+
+
+def test_first_calls_from_several_threads():
+    """A process whose threads make the first call of every kernel side by side, each on its own stream."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here), os.environ.get("PYTHONPATH", "")]))
+    r = subprocess.run([sys.executable, "-c", THREADS], env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
