@@ -1083,9 +1083,9 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                         mma_ts<true>(d, tile, v, kO);
 #pragma unroll
                     for (int s = 1; s < kTile / 16; ++s) mma_ts<true>(d, tile + s * 8, v + s * (2 * D * 16 >> 4), kO);
-                    commit(&sm.odone[m]);
-                    if (j + 1 == wk.n_tile) commit(&sm.olast[m]);
-                    commit(&sm.vempty[vs]);
+                    // (Only barriers that someone waits for: an arrival at one that nobody does could come after the CTA's end.)
+                    commit(j + 1 == wk.n_tile ? &sm.olast[m] : &sm.odone[m]);
+                    if (j + kStages < wk.n_tile) commit(&sm.vempty[vs]);
                 }
                 if (ahead >= wk.n_tile) continue;
                 ok = reached(&sm.kfull[ks], (ahead / kStages) & 1);
@@ -1096,7 +1096,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
 #pragma unroll
                 for (int s = 1; s < D / 16; ++s) mma_ss<true>(tile, qd + s * (2 * kQueryPitch >> 4), k + s * (2 * kKeyPitch >> 4), kS);
                 commit(&sm.sfull[m][j & 1]);
-                commit(&sm.kempty[ks]);
+                if (ahead + kStages < wk.n_tile) commit(&sm.kempty[ks]);
             }
         }
     }
