@@ -374,6 +374,14 @@ def _need_rows(q, name: str, rows: Optional[int], heads: int, d: int):
     return q.data_ptr(), _dtype_code(q), shape[0], stride[0] if shape[0] > 1 else heads * d, dev
 
 
+def _count(v, name: str) -> int:
+    """A C int that is not negative (ctypes would drop the upper bits of a larger number)."""
+    v = int(v)
+    if not 0 <= v <= 0x7fffffff:
+        raise ValueError(f"{name} must be from 0 to 2147483647, got {v}")
+    return v
+
+
 # the current stream's handle without a torch.cuda.Stream around it, where torch has it
 _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -390,10 +398,11 @@ def kvq_sink_decode_attention(layout: Layout, cache: PagedCache, q: torch.Tensor
     """kvq.h kvq_sink_decode_attention: q [B][Hq][d] (rows may lie apart) -> out bf16 [B][Hq][d], lse fp32 [B][Hq];
     the query of a sequence sees its first `sinks` and its newest `span` cached positions."""
     B, Hq, d = cache.batch, layout.num_q_heads, layout.head_dim
+    max_len, sinks, span = _count(max_len, "max_len"), _count(sinks, "sinks"), _count(span, "span")
     qp, qt, _, stride, dev = _need_rows(q, "q", B, Hq, d)
     rc = lib().kvq_sink_decode_attention(
-        C.byref(layout.c()), C.byref(cache.c()), qp, qt, stride, _need(lens, "lens", _I32, B, dev), int(max_len),
-        int(sinks), int(span), sm_scale, _need(out, "out", _BF16, B * Hq * d, dev),
+        C.byref(layout.c()), C.byref(cache.c()), qp, qt, stride, _need(lens, "lens", _I32, B, dev), max_len,
+        sinks, span, sm_scale, _need(out, "out", _BF16, B * Hq * d, dev),
         _need(lse, "lse", _F32, B * Hq, dev, True), _stream_of(stream, dev))
     if rc != KVQ_OK:
         raise KVQError("kvq_sink_decode_attention", rc)
@@ -406,12 +415,13 @@ def kvq_sink_prefill_attention(layout: Layout, cache: PagedCache, q: torch.Tenso
     q [total_q][Hq][d], rows may lie apart), causal, over its first `sinks` positions and the newest `span`
     positions up to each query -> out bf16 [total_q][Hq][d], lse fp32 [total_q][Hq]."""
     B, Hq, d = cache.batch, layout.num_q_heads, layout.head_dim
+    max_q, sinks, span = _count(max_q, "max_q"), _count(sinks, "sinks"), _count(span, "span")
     qp, qt, T, stride, dev = _need_rows(q, "q", None, Hq, d)
     if T == 0:                                   # nothing to do (an empty tensor has no address)
         return
     rc = lib().kvq_sink_prefill_attention(
         C.byref(layout.c()), C.byref(cache.c()), qp, qt, stride, _need(cu_q, "cu_q", _I32, B + 1, dev),
-        _need(lens, "lens", _I32, B, dev), int(max_q), int(sinks), int(span), sm_scale,
+        _need(lens, "lens", _I32, B, dev), max_q, sinks, span, sm_scale,
         _need(out, "out", _BF16, T * Hq * d, dev), _need(lse, "lse", _F32, T * Hq, dev, True), _stream_of(stream, dev))
     if rc != KVQ_OK:
         raise KVQError("kvq_sink_prefill_attention", rc)
@@ -422,6 +432,7 @@ def kvq_read_back(layout: Layout, cache: PagedCache, first: torch.Tensor, cu_row
     """kvq.h kvq_read_back: positions first[b], first[b] + 1, ... of every sequence as rows
     cu_rows[b]..cu_rows[b+1] of k_out and v_out [rows][Hkv][d] (bf16 or fp32), keys in the model's basis."""
     B, row = cache.batch, layout.num_kv_heads * layout.head_dim
+    max_rows = _count(max_rows, "max_rows")
     if k_out.dtype != v_out.dtype:
         raise ValueError("k_out and v_out must share a dtype")
     n = k_out.numel()
@@ -433,7 +444,7 @@ def kvq_read_back(layout: Layout, cache: PagedCache, first: torch.Tensor, cu_row
     kp, vp = _need(k_out, "k_out", _FLOAT_IN, n, dev), _need(v_out, "v_out", _FLOAT_IN, n, dev)
     rc = lib().kvq_read_back(
         C.byref(layout.c()), C.byref(cache.c()), _need(first, "first", _I32, B, dev),
-        _need(cu_rows, "cu_rows", _I32, B + 1, dev), _need(lens, "lens", _I32, B, dev), int(max_rows), kp, vp,
+        _need(cu_rows, "cu_rows", _I32, B + 1, dev), _need(lens, "lens", _I32, B, dev), max_rows, kp, vp,
         _dtype_code(k_out), _stream_of(stream, dev))
     if rc != KVQ_OK:
         raise KVQError("kvq_read_back", rc)
