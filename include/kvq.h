@@ -368,8 +368,13 @@ int kvq_dequantize(const kvq_layout* layout, const kvq_cache* cache,
  *    [Hq] (natural log) or NULL.
  *  - Scores, softmax statistics and sums are fp32; out is rounded to bf16
  *    once.  Single tokens over key groups of 32 channels or more multiply the
- *    codes themselves: out is within 1e-3 + 1e-3*|o| (+ its rounding) and lse
- *    within 1e-3 + 1e-3*|lse| of the same sums in fp64.  Chunks, and single
+ *    codes themselves, and scores and lse are fp32's.  A weight is rounded to
+ *    fp16, and its product with a value's scale again: out is off by at most
+ *        2^-11 sum a (|v| + |code*scale|)
+ *        + 2^(s-36) a_max sum (|code*scale| + |zero| + c)
+ *    over the visible positions, where a_max is the largest weight, every value
+ *    scale is below 2^s (s >= 0) and c = 129, 771, 255, 255 for 1, 2, 4, 8 bits
+ *    (values around one: within 1e-3 + 1e-3*|o| as measured).  Chunks, and single
  *    tokens of the other layouts, round keys and values to fp16 (and queries
  *    that are fp32 or rotated), each by up to 2^-11 of itself or 2^-25, the
  *    larger: a score is off by at most

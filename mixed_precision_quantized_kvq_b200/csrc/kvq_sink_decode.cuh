@@ -211,7 +211,10 @@ struct Sums {
 template <int D>
 __device__ __forceinline__ void raise_ref(Sums<D>& S, const float (&top)[2], int log_scale) {
     // Weights are 2^(score - ref), at most 2^15, and so are their products with the value scales (below
-    // 2^log_scale): both round to fp16 without overflow, and what lies 2^-39 below the largest still counts.
+    // 2^log_scale): both round to fp16 without overflow, by up to 2^-11 of themselves.  After a rise the largest weight is
+    // 2^(11 - log_scale), so half a step of the smallest fp16 numbers, 2^-25, is 2^(log_scale - 36) of it: that much of
+    // a weight, and of a product times its code and 2^value_bit (divided out of it, a rounding of its own), may be lost.
+    // log_scale is the largest over a page's groups: one group of large scales takes range from the others.
     const float need0 = top[0] - 15.f + float(log_scale), need1 = top[1] - 15.f + float(log_scale);
     if (__any_sync(kAll, need0 > S.ref[0] || need1 > S.ref[1])) {
         // four binades of room, so that the next rise seldom comes soon
@@ -366,6 +369,7 @@ __device__ __forceinline__ void page_values(const Params& p, unsigned char* sv, 
     for (int i = lane; i < kPage * nvg; i += 32) vmax = max(vmax, lds32(svm + i * 4) & 0x7fffu);
     vmax = __reduce_max_sync(kAll, vmax);
     raise_ref(S, top, max(0, int(vmax >> 10) - 14));     // a scale is below 2^(exponent field - 14)
+    // (l sums the weights before they are rounded: lse is fp32's, and an output keeps the roundings of its weights)
     uint32_t w[8];                                       // weights of pair T, head r
 #pragma unroll
     for (int T = 0; T < 8; ++T) {

@@ -1,5 +1,5 @@
 """The attention with sinks at its edges, against fp64 numpy over the oracle's cache: clusters whose CTAs have no
-tile, weights far below the largest, queries with NaN, first calls from several threads."""
+tile, weights far below the largest, value scales far apart, queries with NaN, first calls from several threads."""
 import os
 import subprocess
 import sys
@@ -130,6 +130,48 @@ def test_one_page_far_above_the_others(layout, form, low, high):
     want, want_lse = ref.attention(pair.ocache, pair.pt, None, q.astype(np.float64), n, pair.lens, 64, INF, scale)
     tol = (2.0 ** -11 + 2.0 ** -12 + 2.0 ** -14) * want + 2.0 ** -33 * np.exp(-want_lse)[:, :, None] * val.sum()
     ref.check_bf16(out.float().cpu().numpy(), want, tol=tol)
+    ref.check_lse(lse.cpu().numpy(), want_lse, np.full(want_lse.shape, 2.0 ** -14))
+
+
+
+@pytest.mark.parametrize("large", [0, 7])
+@pytest.mark.parametrize("vb,vg,d", [(1, 32, 128), (2, 32, 128), (4, 16, 128), (8, 64, 128), (2, 16, 64), (8, 32, 64)])
+def test_value_groups_of_different_scales(vb, vg, d, large):
+    """Single tokens over exact codes: values of the first group around 2^large and of the others around 2^-6, weights from
+    1 down to 2^-24.  Keys and queries as above (scores are exact).  The bound of the two roundings to fp16, of a weight
+    and of its product with the scale, and of fp32 sums over 64 pages of 4 products at 2^-23 each (2^-15, and as much
+    again for the rest):
+        2^-11 sum a (|v| + |code*scale|) + 2^-14 sum a (|code*scale| + |zero|)
+        + 2^(s-36) a_max sum (|code*scale| + |zero| + c)"""
+    w = small(batch=1, num_kv_heads=1, num_q_heads=3, head_dim=d, v_bits=vb, v_group=vg)
+    L, r = 4096, np.random.default_rng(7)
+    key = np.repeat(-r.integers(10 * 8, 24 * 8, L // 64) / 8.0, 64)
+    key[:64] = 0.0
+    val = r.standard_normal((L, d)) * np.where(np.arange(d) < vg, 2.0 ** large, 2.0 ** -6)
+    val[:64] *= 2.0 ** -4                                     # the largest weights' values do not hide the others'
+    pair = Pair(w, np.array([L], np.int32))
+    pair.lens[:] = 0
+    pair.glens.zero_()
+    pair.append(wl.bf16_bits(np.repeat(key.astype(np.float32), d).reshape(L, 1, d)),
+                wl.bf16_bits(val.astype(np.float32).reshape(L, 1, d)), np.array([0, L]))
+    pair.compare_cache()
+    q = np.zeros((1, 3, d), np.float32)
+    q[:, :, 3] = 1.0
+    out, lse = kvq.sink_decode_attention(pair.glay, pair.gcache, torch_raw(wl.bf16_bits(q)), pair.glens, L, 64, INF,
+                                         float(np.log(2.0)))
+    want, want_lse = ref.attention(pair.ocache, pair.pt, None, q.astype(np.float64), np.ones(1, int), pair.lens, 64, INF,
+                                   float(np.log(2.0)))
+    v = pair.ocache.dequantize(pair.lens, L)[1][0, 0].astype(np.float64)
+    groups = v.reshape(L, d // vg, vg)
+    zero = np.repeat(groups.min(-1), vg, -1)                  # code 0 is a group's smallest value
+    s = max(0.0, np.ceil(np.log2((groups.max(-1) - groups.min(-1)).max() / (2 ** vb - 1)) + 1e-3))
+    code = v - zero
+    a = np.exp(key * np.log(2.0))
+    a /= a.sum()
+    c = {1: 129, 2: 771, 4: 255, 8: 255}[vb]
+    tol = (2.0 ** -11 * (a @ (np.abs(v) + code)) + 2.0 ** -14 * (a @ (code + np.abs(zero)))
+           + 2.0 ** (s - 36) * a.max() * (code + np.abs(zero) + c).sum(0))
+    ref.check_bf16(out.float().cpu().numpy()[0], want[0], tol=np.broadcast_to(tol, want[0].shape))
     ref.check_lse(lse.cpu().numpy(), want_lse, np.full(want_lse.shape, 2.0 ** -14))
 
 
