@@ -192,7 +192,7 @@ __device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_ca
 // mantissa of 1024 + code * 2^position; one exact operation takes both away.
 template <int BITS>
 __device__ __forceinline__ void unpack(uint32_t w, __half2 (&c)[16 / BITS]) {
-    constexpr int kSpan = 10 / BITS * BITS < 10 ? (BITS == 4 ? 8 : 8) : 10;
+    constexpr int kSpan = 10 / BITS * BITS;              // whole codes among the ten bits
     constexpr uint32_t kMask = ((1u << BITS) - 1u) * 0x00010001u;
 #pragma unroll
     for (int i = 0; i < 16 / BITS; ++i) {
@@ -1127,7 +1127,10 @@ cudaError_t launch_d(const Params& p, const Args& a, int sms, unsigned* status, 
     }
     static_assert(2 * kRows * kPartPitch<D> * 4 <= int(offsetof(Smem<D>, vscale)), "a join's part lies over the operands");
     const int per = 2 * (kRows / p.g), blocks = (a.max_q - 1) / per + 1;
-    // CTAs that share the tiles of a block of rows: as many as there are SMs for, with four tiles each at least
+    // CTAs that share the tiles of a block of rows: as many as there are SMs for, with four tiles each at least if a
+    // sequence fills the page table.  (Lengths are on the device: a shorter sequence leaves some without a tile and joins
+    // empty parts.  Eight kv-heads, 100 positions: 33 queries take 18 us and 100 queries 38 under a table of 512 pages, 12
+    // and 13 under one of 2 pages, where nothing is shared.)
     const long long cached = std::min<long long>((long long)p.max_pages * kPage + ring_slots(p, a.kpc), a.len_cap);
     const long long tiles = std::min(cached, (long long)a.sinks + a.span + per + 2 * kPage) / kTile;
     const long long all = (long long)blocks * p.hkv * p.batch;
