@@ -382,6 +382,26 @@ def _count(v, name: str) -> int:
     return v
 
 
+def _need_cache(layout: Layout, cache: PagedCache, dev: int) -> kvq_cache:
+    """PagedCache.c() of a cache whose buffers and page table (int32) are, as the layout's signs, on the call's device."""
+    table, signs, at = cache.page_table, layout.rot_signs, []
+    for t in (cache.k_codes, cache.v_codes, cache.k_meta, cache.v_meta, cache.k_win, cache.v_win, table):
+        if t is None:
+            at.append(None)
+        elif t.get_device() == dev and t.is_contiguous():
+            at.append(t.data_ptr())
+        elif t.get_device() != dev:
+            raise ValueError(f"a buffer of the cache is on {t.device}, not on the current CUDA device cuda:{dev}")
+        else:
+            raise ValueError("tensor must be contiguous")
+    if table.dtype is not torch.int32:
+        raise ValueError(f"page_table must have dtype torch.int32, got {table.dtype}")
+    if signs is not None and signs.get_device() != dev:
+        raise ValueError(f"rot_signs is on {signs.device}, not on the current CUDA device cuda:{dev}")
+    shape = table.shape
+    return kvq_cache(*at, shape[0], shape[1], int(cache.num_pages))
+
+
 # the current stream's handle without a torch.cuda.Stream around it, where torch has it
 _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -400,8 +420,9 @@ def kvq_sink_decode_attention(layout: Layout, cache: PagedCache, q: torch.Tensor
     B, Hq, d = cache.batch, layout.num_q_heads, layout.head_dim
     max_len, sinks, span = _count(max_len, "max_len"), _count(sinks, "sinks"), _count(span, "span")
     qp, qt, _, stride, dev = _need_rows(q, "q", B, Hq, d)
+    cc = _need_cache(layout, cache, dev)
     rc = lib().kvq_sink_decode_attention(
-        C.byref(layout.c()), C.byref(cache.c()), qp, qt, stride, _need(lens, "lens", _I32, B, dev), max_len,
+        C.byref(layout.c()), C.byref(cc), qp, qt, stride, _need(lens, "lens", _I32, B, dev), max_len,
         sinks, span, sm_scale, _need(out, "out", _BF16, B * Hq * d, dev),
         _need(lse, "lse", _F32, B * Hq, dev, True), _stream_of(stream, dev))
     if rc != KVQ_OK:
@@ -419,8 +440,9 @@ def kvq_sink_prefill_attention(layout: Layout, cache: PagedCache, q: torch.Tenso
     qp, qt, T, stride, dev = _need_rows(q, "q", None, Hq, d)
     if T == 0:                                   # nothing to do (an empty tensor has no address)
         return
+    cc = _need_cache(layout, cache, dev)
     rc = lib().kvq_sink_prefill_attention(
-        C.byref(layout.c()), C.byref(cache.c()), qp, qt, stride, _need(cu_q, "cu_q", _I32, B + 1, dev),
+        C.byref(layout.c()), C.byref(cc), qp, qt, stride, _need(cu_q, "cu_q", _I32, B + 1, dev),
         _need(lens, "lens", _I32, B, dev), max_q, sinks, span, sm_scale,
         _need(out, "out", _BF16, T * Hq * d, dev), _need(lse, "lse", _F32, T * Hq, dev, True), _stream_of(stream, dev))
     if rc != KVQ_OK:
@@ -442,8 +464,9 @@ def kvq_read_back(layout: Layout, cache: PagedCache, first: torch.Tensor, cu_row
     if n % row:
         raise ValueError(f"k_out must hold whole rows of {row} elements ([rows][Hkv][d])")
     kp, vp = _need(k_out, "k_out", _FLOAT_IN, n, dev), _need(v_out, "v_out", _FLOAT_IN, n, dev)
+    cc = _need_cache(layout, cache, dev)
     rc = lib().kvq_read_back(
-        C.byref(layout.c()), C.byref(cache.c()), _need(first, "first", _I32, B, dev),
+        C.byref(layout.c()), C.byref(cc), _need(first, "first", _I32, B, dev),
         _need(cu_rows, "cu_rows", _I32, B + 1, dev), _need(lens, "lens", _I32, B, dev), max_rows, kp, vp,
         _dtype_code(k_out), _stream_of(stream, dev))
     if rc != KVQ_OK:

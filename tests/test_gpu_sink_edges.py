@@ -1,5 +1,6 @@
 """The attention with sinks at its edges, against fp64 numpy over the oracle's cache: clusters whose CTAs have no
-tile, weights far below the largest, value scales far apart, queries with NaN, first calls from several threads."""
+tile, weights far below the largest, value scales far apart, queries with NaN, caches that are
+elsewhere, first calls from several threads."""
 import os
 import subprocess
 import sys
@@ -204,6 +205,35 @@ def test_a_query_with_nan(layout, form):
     assert torch.equal(got[~bad], out[~bad]) and torch.equal(got_lse[~bad], lse[~bad])
     got, got_lse = call(0)
     assert torch.all(got == 0) and torch.all(got_lse == -float("inf"))
+
+
+
+# ---------------------------------------------------------------- refused on the host
+
+@pytest.mark.parametrize("name", ["page_table", "k_codes", "v_codes", "k_meta", "v_meta", "k_win", "v_win", "rot_signs"])
+def test_a_cache_on_another_device(name):
+    """A buffer of the cache in host memory, or a page table of 64-bit numbers, is refused before anything is launched."""
+    w = small(batch=2, rotate_keys=True, window=40)
+    pair = build(w, [100, 90])
+    q, cu = torch_raw(ref.queries(w, 2)[0]), i32([0, 1, 2])
+
+    def refused(match):
+        with pytest.raises(ValueError, match=match):
+            kvq.sink_decode_attention(pair.glay, pair.gcache, q, pair.glens, 100, 4, 50)
+        with pytest.raises(ValueError, match=match):
+            kvq.sink_prefill_attention(pair.glay, pair.gcache, q, cu, pair.glens, 1, 4, 50)
+        with pytest.raises(ValueError, match=match):
+            kvq.read_back(pair.glay, pair.gcache, i32([0, 0]), cu, pair.glens, 2, 1)
+
+    holder = pair.glay if name == "rot_signs" else pair.gcache
+    kept = getattr(holder, name)
+    setattr(holder, name, kept.cpu())
+    refused("is on cpu")
+    if name == "page_table":
+        setattr(holder, name, kept.long())
+        refused("int32")
+    setattr(holder, name, kept)
+    kvq.sink_decode_attention(pair.glay, pair.gcache, q, pair.glens, 100, 4, 50)
 
 
 # ---------------------------------------------------------------- threads
