@@ -385,6 +385,9 @@ int kvq_dequantize(const kvq_layout* layout, const kvq_cache* cache,
  *    2^-25 and by 2^-33 a_max sum |v| over the visible positions.  There
  *    reconstructed keys and values must lie within +-65504: a value beyond, or
  *    NaN, reaches its channel of the chunk's other queries.
+ *  - Lengths up to 2^31 - 1024.  A chunk's launch is sized by the width of the
+ *    page table (lengths are on the device): under a table far wider than a
+ *    short chunk needs, its call takes up to 25 us longer.
  *  - No workspace; calls on different streams may overlap as long as no
  *    call writes the cache.  Results do not depend on what else runs. */
 

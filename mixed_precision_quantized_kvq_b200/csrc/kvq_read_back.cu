@@ -14,9 +14,10 @@
 // along positions (values, keys with groups along positions) are read as one
 // word of eight channels each, for D/16 neighbouring positions.  Measured on a
 // B200: 88 us for 4096 rows of 16 sequences and 8 heads in bf16 (336 MB, 3.8
-// TB/s); the issue slots of the reconstruction (about 70 for a warp's 256
-// channels) are what is left above the bytes.  Keys and values of a page in one
-// CTA took 96.
+// TB/s, 58% of the copy rate).  Issue slots (about 70 for the reconstruction of
+// a warp's 256 channels) are 42% busy: what is left above the bytes is a CTA's
+// chain of loads (rows, first position, length, page number, codes).  Keys and
+// values of a page in one CTA took 96.
 #include "kvq_sink.cuh"
 
 namespace kvq {

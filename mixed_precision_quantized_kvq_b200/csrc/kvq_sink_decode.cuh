@@ -10,17 +10,22 @@
 // The power of two of its position is divided out of the other operand, 2^24
 // out of the result.  One mask per two codes is all the unpacking there is.
 //
-// What bounds it: the codes and metadata of the visible positions in (116
-// bytes per position and kv-head for 4-bit keys and 2-bit values), and about
-// 1100 issue slots a warp for 64 of them, which at this many bytes is the
-// larger part.  Hence the products on mma.sync.m16n8k16 with the positions
+// What bounds it: latency.  It has to read the codes and metadata of the
+// visible positions (116 bytes per position and kv-head for 4-bit keys and
+// 2-bit values) and to issue about 1100 instructions a warp for 64 of them, and
+// at the size below the two take about as long.  Hence the products on
+// mma.sync.m16n8k16 with the positions
 // (scores) or channels (values) as its 16 rows and the up to 8 query heads of
 // a kv-head as its 8 columns: fragments are registers, the codes never go
 // through shared memory a second time.  Measured on a B200: 28.8 us for 16
 // sequences of 32 query and 8 kv-heads over 4096 positions (67.6 MB, 10.3 us at
-// the copy rate), of which about 9 are start-up (dependent loads of length,
-// page table and codes, first fetch of the instructions, the join); 9.3 MB more
-// cost 2.5 us, 56% of the copy rate.
+// the copy rate): 12.5 whatever the span (dependent loads of length, page table
+// and codes, first fetch of the instructions, the ring, the join) and 4.05 for
+// each 1024 positions, 56% of the copy rate, up to a span of 16384.  Issue slots
+// are 48% busy and DRAM 29%: 16 warps with a stage each for keys and for values do not
+// cover the latency of a page.  Rotated keys and fp32 queries add a low part
+// of the query, whose fragments make the head_dim-128 builds spill (84 to 124
+// bytes a thread at 128 registers).
 //
 // Work split: one cluster of 1 to 16 CTAs per (sequence, kv-head); its warps
 // take the 64-position pages in turn (warp w of W: pages w, w + W, ...), then

@@ -1,17 +1,20 @@
 // Attention of a chunk of new queries with sinks and a sliding span over the
 // quantized cache (kvq_sink_prefill_attention) on the 5th-generation tensor
 // cores (tcgen05, sm_100a).  Every layout; also the single-token form of the
-// layouts whose scales are not shared by 32 channels (kvq_sink_decode.cuh).
+// layouts whose scales are not shared by 32 channels (kvq_sink_decode.cuh): up
+// to 8 of its 256 rows; one sequence, 8192 positions: 37 us with key groups
+// along positions, 33 with groups of 16 channels.
 //
 //     S = Q K^T,  P = 2^(factor S - ref) where visible,  O += P V,  l += P 1
 //
 // over tiles of 64 positions (a page), with a running reference exponent per
 // query row; O / l is rounded to bf16.  Bound by the tensor cores and the
 // exponentials (one per visible pair: 16 a clock and SM, which takes as long as
-// the two products at head_dim 128), in practice by the issue slots and the
-// hand-overs of a tile.  Measured on a B200: 738 us for chunks of 512 queries of
-// 16 sequences at 4096 positions, 32 query and 8 kv-heads (550 GFLOP: 745
-// TFLOP/s, 45% of a library product's rate); a tile takes 2.4 us a CTA of which
+// the two products at head_dim 128), in practice by the hand-overs of a tile:
+// the tensor core works 46% of the time, issue slots are 62% busy, exponentials
+// 35%.  Measured on a B200: 749 us for chunks of 512 queries of
+// 16 sequences at 4096 positions, 32 query and 8 kv-heads (550 GFLOP: 735
+// TFLOP/s, 44% of a library product's rate); a tile takes 2.4 us a CTA of which
 // the tensor core works 0.7, a CTA's start and end about 15.
 //
 // One CTA per SM takes 256 rows of one (sequence, kv-head): two blocks of 128,
@@ -35,7 +38,7 @@
 // Where few rows leave SMs idle and there are tiles enough, a cluster of 2, 4 or
 // 8 CTAs shares the tiles of its rows (CTA c of n: tiles c, c + n, ...) and joins
 // its outputs through distributed shared memory: 33 queries over 16000 positions
-// of one sequence take 68 us.  A kernel of its own, since the arithmetic of the
+// of one sequence take 66 us.  A kernel of its own, since the arithmetic of the
 // shared tiles costs the others 8%.
 // Operands are 8x16-byte core matrices without swizzle, all 16-byte pieces of
 // the same eight columns together, which makes the writers' 16-byte stores
@@ -765,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                     unpack2(fma2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), f2, r2), x, y);
                     x = ex2(x);
                     y = ex2(y);
-                    part[i & 3] += x + y;
+                    part[i & 3] += x + y;                 // (before they are rounded: lse is fp32's)
                     s[0][i] = bits(__floats2half2_rn(x, y));   // (slot i has been read)
                 }
                 tmem_st32(ts, s[0]);                      // over S
