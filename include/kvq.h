@@ -374,17 +374,20 @@ int kvq_dequantize(const kvq_layout* layout, const kvq_cache* cache,
  *        + 2^(s-36) a_max sum (|code*scale| + |zero| + c)
  *    over the visible positions, where a_max is the largest weight, every value
  *    scale is below 2^s (s >= 0) and c = 129, 771, 255, 255 for 1, 2, 4, 8 bits
- *    (values around one: within 1e-3 + 1e-3*|o| as measured).  Chunks, and single
- *    tokens of the other layouts, round keys and values to fp16 (and queries
+ *    (values around one: within 1e-3 + 1e-3*|o| as measured).  Single tokens of
+ *    the other layouts take keys and queries as two fp16 numbers each, to 2^-22
+ *    of themselves or 2^-25, so that scores and lse are fp32's too; values and
+ *    weights as below.  Chunks round keys and values to fp16 (and queries
  *    that are fp32 or rotated), each by up to 2^-11 of itself or 2^-25, the
  *    larger: a score is off by at most
  *        D = |sm_scale| sum_j |q_j| (2^-11 |k_j| + 2^-25)
  *    (2^-10 with the query's rounding) and lse by D.  Weights are rounded to
  *    fp16 too, by up to 2^-11 of themselves or 2^-33 of the largest: out is
- *    off by a factor within exp(+-2D) of each weight, by 2^-10 sum a |v| +
- *    2^-25 and by 2^-33 a_max sum |v| over the visible positions.  There
- *    reconstructed keys and values must lie within +-65504: a value beyond, or
- *    NaN, reaches its channel of the chunk's other queries.
+ *    off by a factor within exp(+-2D) of each weight (D = 0 for single
+ *    tokens), by 2^-10 sum a |v| + 2^-25 and by 2^-33 a_max sum |v| over the
+ *    visible positions.  There reconstructed keys and values must lie within
+ *    +-65504: a value beyond, or NaN, reaches its channel of the chunk's
+ *    other queries.
  *  - Lengths up to 2^31 - 1024.  A chunk's launch is sized by the width of the
  *    page table (lengths are on the device): under a table far wider than a
  *    short chunk needs, its call takes up to 25 us longer.

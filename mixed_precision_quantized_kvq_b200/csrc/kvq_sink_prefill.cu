@@ -2,8 +2,8 @@
 // quantized cache (kvq_sink_prefill_attention) on the 5th-generation tensor
 // cores (tcgen05, sm_100a).  Every layout; also the single-token form of the
 // layouts whose scales are not shared by 32 channels (kvq_sink_decode.cuh): up
-// to 8 of its 256 rows; one sequence, 8192 positions: 37 us with key groups
-// along positions, 33 with groups of 16 channels.
+// to 8 of its 256 rows; one sequence, 8192 positions: 46 us with key groups
+// along positions, 41 with groups of 16 channels.
 //
 //     S = Q K^T,  P = 2^(factor S - ref) where visible,  O += P V,  l += P 1
 //
@@ -247,12 +247,28 @@ __device__ __forceinline__ void widen(const uint4& w, float (&x)[8]) {
     }
 }
 
+// Two fp32 numbers as their nearest fp16 numbers and what those leave, in fp16 again: together 2^-22 of themselves off,
+// or half a step of the smallest fp16 numbers.
+struct Split {
+    uint32_t high, low;
+};
+__device__ __forceinline__ Split split2(float x, float y) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return {bits(h), bits(__floats2half2_rn(x - __low2float(h), y - __high2float(h)))};
+}
+// code * scale + zero in fp32, split
+__device__ __forceinline__ Split split_key(__half2 code, __half2 scale, __half2 zero) {
+    return split2(fmaf(__low2float(code), __low2float(scale), __low2float(zero)),
+                  fmaf(__high2float(code), __high2float(scale), __high2float(zero)));
+}
+
 // One row of D channels by D/8 neighbouring lanes, eight channels each, to column `row` of an operand of fp16 pieces
 // `pitch` bytes apart; n: codes per word of the keys (channel order).  scaled: by `sign` and a power of two into
-// [2^13, 2^14); returns that power's inverse.  The whole warp calls it; nothing is stored where `to` is null.
-template <int D>
+// [2^13, 2^14); returns that power's inverse.  EXACT: what the fp16 numbers leave goes `low` bytes further.  The whole warp
+// calls it; nothing is stored where `to` is null.
+template <int D, bool EXACT>
 __device__ __forceinline__ float put_row(float (&x)[8], const int8_t* signs, bool scaled, float sign, unsigned char* to,
-                                         int pitch, int row, int n) {
+                                         int low, int pitch, int row, int n) {
     const int oct = threadIdx.x % (D / 8);
     if (signs) {
 #pragma unroll
@@ -288,17 +304,29 @@ __device__ __forceinline__ float put_row(float (&x)[8], const int8_t* signs, boo
         down = __uint_as_float(uint32_t(127 - 13 + e) << 23);
     }
     if (!to) return down;
-    if (n <= 8) {                                        // the lane's channels stay in one piece
-        const auto pair = [&](int a, int b) { return bits(__floats2half2_rn(x[a] * up, x[b] * up)); };
-        *reinterpret_cast<uint4*>(to + oct * pitch + row * 16) =
-            n == 8   ? make_uint4(pair(0, 4), pair(1, 5), pair(2, 6), pair(3, 7))
-            : n == 4 ? make_uint4(pair(0, 2), pair(1, 3), pair(4, 6), pair(5, 7))
-                     : make_uint4(pair(0, 1), pair(2, 3), pair(4, 5), pair(6, 7));
-    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int s = slot_of(oct * 8 + i, n);
-            *reinterpret_cast<__half*>(to + (s >> 3) * pitch + row * 16 + (s & 7) * 2) = __float2half_rn(x[i] * up);
+    for (int part = 0; part < (EXACT ? 2 : 1); ++part) {
+        if (n <= 8) {                                    // the lane's channels stay in one piece
+            const auto pair = [&](int a, int b) { return bits(__floats2half2_rn(x[a] * up, x[b] * up)); };
+            *reinterpret_cast<uint4*>(to + oct * pitch + row * 16) =
+                n == 8   ? make_uint4(pair(0, 4), pair(1, 5), pair(2, 6), pair(3, 7))
+                : n == 4 ? make_uint4(pair(0, 2), pair(1, 3), pair(4, 6), pair(5, 7))
+                         : make_uint4(pair(0, 1), pair(2, 3), pair(4, 5), pair(6, 7));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int s = slot_of(oct * 8 + i, n);
+                *reinterpret_cast<__half*>(to + (s >> 3) * pitch + row * 16 + (s & 7) * 2) = __float2half_rn(x[i] * up);
+            }
+        }
+        if (EXACT && part == 0) {
+            to += low;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[i] *= up;
+                x[i] -= __half2float(__float2half_rn(x[i]));
+            }
+            up = 1.f;
         }
     }
     return down;
@@ -339,11 +367,12 @@ __device__ __forceinline__ void load_part(uint4 (&to)[M], const uint8_t* at, int
 
 __device__ __forceinline__ uint32_t word_of(const uint4& q, int w) { return w == 0 ? q.x : w == 1 ? q.y : w == 2 ? q.z : q.w; }
 
-// half the channels (first C0) of a position, codes in `raw`, metadata of their groups, to row `row` of the key tile
-template <int BITS, int D, int KG>
+// half the channels of a position, codes in `raw`, metadata of their groups, to its row of the key tile (LOW bytes further
+// what fp16 leaves of them, unless LOW is 0)
+template <int BITS, int D, int KG, int LOW>
 __device__ __forceinline__ void put_key(const uint4 (&raw)[4], const uint32_t (&meta)[4], unsigned char* to) {
     constexpr int N = 32 / BITS, W = D / 2 / N;          // codes a word, words
-    __half2 out[4];
+    uint32_t out[4], rest[4];
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         // groups of the word's low and high codes
@@ -354,26 +383,33 @@ __device__ __forceinline__ void put_key(const uint4 (&raw)[4], const uint32_t (&
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
             const int s = w * (N / 2) + i;               // pair
-            out[s & 3] = __hfma2(c[i], scale, zero);
-            if ((s & 3) == 3)
-                *reinterpret_cast<uint4*>(to + (s >> 2) * kKeyPitch) = make_uint4(bits(out[0]), bits(out[1]), bits(out[2]), bits(out[3]));
+            if (LOW) {
+                const Split k = split_key(c[i], scale, zero);
+                out[s & 3] = k.high, rest[s & 3] = k.low;
+            } else {
+                out[s & 3] = bits(__hfma2(c[i], scale, zero));
+            }
+            if ((s & 3) == 3) {
+                *reinterpret_cast<uint4*>(to + (s >> 2) * kKeyPitch) = make_uint4(out[0], out[1], out[2], out[3]);
+                if (LOW) *reinterpret_cast<uint4*>(to + LOW + (s >> 2) * kKeyPitch) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+            }
         }
     }
 }
-template <int BITS, int D>
+template <int BITS, int D, int LOW>
 __device__ __forceinline__ void put_key_of(int kg, const uint4 (&raw)[4], const uint32_t (&meta)[4], unsigned char* to) {
-    if (kg == 16)
-        put_key<BITS, D, 16>(raw, meta, to);
+    if (kg == 16 || LOW)                                 // (single tokens over wider groups take the other kernel)
+        put_key<BITS, D, 16, LOW>(raw, meta, to);
     else if (kg == 32 || D == 64)
-        put_key<BITS, D, 32>(raw, meta, to);             // (D = 64: half a row is one group of 32 or part of one of 64)
+        put_key<BITS, D, 32, LOW>(raw, meta, to);        // (D = 64: half a row is one group of 32 or part of one of 64)
     else
-        put_key<BITS, D, 64>(raw, meta, to);             // half a row is one group of 64 or half of one of 128
+        put_key<BITS, D, 64, LOW>(raw, meta, to);        // half a row is one group of 64 or half of one of 128
 }
 
 // Keys with groups along positions: codes of channels 2*cp (raw[0..1]) and 2*cp + 1 (raw[2..3]) at half the positions of a
 // page, 32 from t0 on, to rows of the key tile.  ALL: every one of them lives in the page (a check at each store instead:
-// 564 us against 282 for two prompts of 3000 positions).
-template <int BITS, int D, bool ALL>
+// 564 us against 282 for two prompts of 3000 positions).  LOW: as above.
+template <int BITS, int D, bool ALL, int LOW>
 __device__ __forceinline__ void put_key_pairs(const uint4 (&raw)[4], const uint32_t* meta, int kshift, int t0, int valid, int vn,
                                               unsigned char* to) {
     constexpr int N = 32 / BITS, W = 32 / N;             // codes a word, words a channel
@@ -396,27 +432,31 @@ __device__ __forceinline__ void put_key_pairs(const uint4 (&raw)[4], const uint3
         for (int i = 0; i < N; ++i) {
             const int h = i >= N / 2, t = w * N + i;
             const __half2 c = half2_of(__byte_perm(bits(ca[i % (N / 2)]), bits(cb[i % (N / 2)]), h ? 0x7632 : 0x5410));
-            const __half2 k = __hfma2(c, scale[N > 16 ? h : 0], zero[N > 16 ? h : 0]);
+            const Split k = LOW ? split_key(c, scale[N > 16 ? h : 0], zero[N > 16 ? h : 0])
+                                : Split{bits(__hfma2(c, scale[N > 16 ? h : 0], zero[N > 16 ? h : 0])), 0u};
             int off = 0;
 #pragma unroll
             for (int b = 0; b < 5; ++b)
                 if (t & (1 << b)) off += step[b];
-            if (ALL || t0 + t < valid) *reinterpret_cast<uint32_t*>(to + off) = bits(k);
+            if (ALL || t0 + t < valid) {
+                *reinterpret_cast<uint32_t*>(to + off) = k.high;
+                if (LOW) *reinterpret_cast<uint32_t*>(to + LOW + off) = k.low;
+            }
         }
     }
 }
 
-template <int BITS, int D>
+template <int BITS, int D, int LOW>
 __device__ __forceinline__ void put_key_pairs_of(const uint4 (&raw)[4], const uint32_t* meta, int kshift, int t0, int valid, int vn,
                                                  unsigned char* to) {
     if (t0 + 32 <= valid)
-        put_key_pairs<BITS, D, true>(raw, meta, kshift, t0, valid, vn, to);
+        put_key_pairs<BITS, D, true, LOW>(raw, meta, kshift, t0, valid, vn, to);
     else
-        put_key_pairs<BITS, D, false>(raw, meta, kshift, t0, valid, vn, to);
+        put_key_pairs<BITS, D, false, LOW>(raw, meta, kshift, t0, valid, vn, to);
 }
 
-// half a ring row to its row of the key tile, in the channel order of words of N codes
-template <int N, int D>
+// half a ring row to its row of the key tile, in the channel order of words of N codes.  LOW: as above.
+template <int N, int D, int LOW>
 __device__ __forceinline__ void put_ring_key(const __nv_bfloat16* src, unsigned char* to) {
     constexpr int C = N > 8 ? N : 8;                     // channels that are exchanged among themselves
 #pragma unroll 2
@@ -428,16 +468,22 @@ __device__ __forceinline__ void put_ring_key(const __nv_bfloat16* src, unsigned 
             u[4 * i] = v.x, u[4 * i + 1] = v.y, u[4 * i + 2] = v.z, u[4 * i + 3] = v.w;
         }
         const auto at = [&](int ch) { return __uint_as_float(ch & 1 ? u[ch / 2] & 0xffff0000u : u[ch / 2] << 16); };
-        uint32_t out[C / 2];
+        uint32_t out[C / 2], rest[C / 2];
 #pragma unroll
         for (int q = 0; q < C / 2; ++q) {
-            const int low = pair_low<N>(q);
-            out[q] = bits(__floats2half2_rn(at(low), at(low + N / 2)));
+            const int first = pair_low<N>(q);
+            const Split k = LOW ? split2(at(first), at(first + N / 2))
+                                : Split{bits(__floats2half2_rn(at(first), at(first + N / 2))), 0u};
+            out[q] = k.high, rest[q] = k.low;
         }
 #pragma unroll
-        for (int i = 0; i < C / 8; ++i)
+        for (int i = 0; i < C / 8; ++i) {
             *reinterpret_cast<uint4*>(to + (c0 / 8 + i) * kKeyPitch) =
                 make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+            if (LOW)
+                *reinterpret_cast<uint4*>(to + LOW + (c0 / 8 + i) * kKeyPitch) =
+                    make_uint4(rest[4 * i], rest[4 * i + 1], rest[4 * i + 2], rest[4 * i + 3]);
+        }
     }
 }
 
@@ -551,7 +597,11 @@ __device__ __forceinline__ void put_ring_value(const Work<SPLIT>& wk, const __nv
 
 // KPC: keys with groups along positions (with both forms of the keys in one build, chunks of 512 at 4096 positions took 752
 // to 780 us against 738, as the compiler laid out the loop of the keys).
-template <int D, bool SPLIT, bool KPC>
+// EXACT: single tokens, whose scores and lse are to be fp32's as in the other kernel of that call: keys and queries as two fp16
+// numbers each, the low parts in the place of the stages 2 and 3 and of block 1's queries, and S = Q K_low (+ Q_low K_high
+// where queries are fp32 or rotated) + Q K_high.  (16 sequences, span 4096: 137 us with groups of 16 channels and 164 with
+// groups along positions; 95 and 117 with fp16 alone, whose lse was off by 1e-4.)
+template <int D, bool SPLIT, bool KPC, bool EXACT>
 __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_constant__ Params p,
                                                                    const __grid_constant__ Args a, int shared_by, unsigned* status) {
     const int ctas = SPLIT ? shared_by : 1;
@@ -581,6 +631,9 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
     wk.first = max(wk.n_sink, wk.lo / kTile);
     const int all_tiles = wk.n_sink + max(0, (wk.p_max + kTile) / kTile - wk.first);
     wk.n_tile = all_tiles > wk.rank ? (all_tiles - wk.rank + ctas - 1) / ctas : 0;
+    constexpr int kKeyStages = EXACT ? kStages / 2 : kStages;
+    constexpr int kLow = EXACT ? kKeyStages * int(sizeof(sm.k[0])) : 0;   // bytes from a key tile to its low part
+    constexpr int kQueryLow = EXACT ? int(sizeof(sm.q[0])) : 0;
     const int kn = KPC ? 2 : 32 / p.kb, vn = 32 / p.vb; // order of the key's channels (2: as they are) and of positions
 
     // ---- set up ----
@@ -685,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                             if (at >= 0) load8(a.q, false, size_t(at) + oct * 8, x);
                         }
                         // (its exchanges come after every lane's read and before any lane's store)
-                        const float down = put_row<D>(x, p.rotate ? p.signs : nullptr, true, sign, sm.q[m], kQueryPitch, rr, kn);
+                        const float down = put_row<D, EXACT>(x, p.rotate ? p.signs : nullptr, true, sign, sm.q[m], kQueryLow, kQueryPitch, rr, kn);
                         const int from = lane - r0;       // to the lane whose row it is
                         const float v = __shfl_sync(0xffffffffu, down, from >= 0 && from < kPer ? from * (D / 8) : 0);
                         if (from >= 0 && from < kPer) factor = scale * v;
@@ -926,8 +979,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
             load();
 #pragma unroll 1
             for (int j = 0; j < wk.n_tile; ++j) {
-                const int st = j % kStages, t0 = wk.tile_start(j), x = t0 + slot;
-                if (j >= kStages) ok = wait(&sm.kempty[st], (j / kStages + 1) & 1);
+                const int st = j % kKeyStages, t0 = wk.tile_start(j), x = t0 + slot;
+                if (j >= kKeyStages) ok = wait(&sm.kempty[st], (j / kKeyStages + 1) & 1);
                 if (!ok) break;
                 unsigned char* sk = sm.k[st];
                 unsigned char* row = sk + slot_of(slot, vn) * 16 + half * (D / 16) * kKeyPitch;
@@ -935,26 +988,26 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                     if (slot < D / 2 && pg >= 0) {
                         const uint32_t* m = p.k_meta + (size_t(pg) * p.hkv + wk.h) * size_t(kPage >> kshift) * D + 2 * slot;
                         unsigned char* col = sk + (slot >> 2) * kKeyPitch + (slot & 3) * 4 + half * (32 * 16);
-                        if (p.kb == 4) put_key_pairs_of<4, D>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
-                        if (p.kb == 8) put_key_pairs_of<8, D>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
-                        if (p.kb == 2) put_key_pairs_of<2, D>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
-                        if (p.kb == 1) put_key_pairs_of<1, D>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
+                        if (p.kb == 4) put_key_pairs_of<4, D, kLow>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
+                        if (p.kb == 8) put_key_pairs_of<8, D, kLow>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
+                        if (p.kb == 2) put_key_pairs_of<2, D, kLow>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
+                        if (p.kb == 1) put_key_pairs_of<1, D, kLow>(raw, m, kshift, half * 32, wk.Lq - t0, vn, col);
                     }
                 } else if (pg >= 0 && x < wk.Lq) {
-                    if (p.kb == 4) put_key_of<4, D>(p.kg, raw, meta, row);
-                    if (p.kb == 8) put_key_of<8, D>(p.kg, raw, meta, row);
-                    if (p.kb == 2) put_key_of<2, D>(p.kg, raw, meta, row);
-                    if (p.kb == 1) put_key_of<1, D>(p.kg, raw, meta, row);
+                    if (p.kb == 4) put_key_of<4, D, kLow>(p.kg, raw, meta, row);
+                    if (p.kb == 8) put_key_of<8, D, kLow>(p.kg, raw, meta, row);
+                    if (p.kb == 2) put_key_of<2, D, kLow>(p.kg, raw, meta, row);
+                    if (p.kb == 1) put_key_of<1, D, kLow>(p.kg, raw, meta, row);
                 }
                 __syncwarp();
                 if (t0 + kTile > wk.Lq && !p.rotate) {    // ring rows
                     if (x >= wk.Lq && x < wk.L) {
                         const __nv_bfloat16* src = p.k_win + ((size_t(wk.b) * p.hkv + wk.h) * R + x % R) * D + half * (D / 2);
-                        if (kn == 8) put_ring_key<8, D>(src, row);
-                        if (kn == 2) put_ring_key<2, D>(src, row);
-                        if (kn == 4) put_ring_key<4, D>(src, row);
-                        if (kn == 16) put_ring_key<16, D>(src, row);
-                        if (kn == 32) put_ring_key<32, D>(src, row);
+                        if (kn == 8) put_ring_key<8, D, kLow>(src, row);
+                        if (kn == 2) put_ring_key<2, D, kLow>(src, row);
+                        if (kn == 4) put_ring_key<4, D, kLow>(src, row);
+                        if (kn == 16) put_ring_key<16, D, kLow>(src, row);
+                        if (kn == 32) put_ring_key<32, D, kLow>(src, row);
                     }
                 } else if (t0 + kTile > wk.Lq) {          // rotated first: D/8 lanes a row, two loads under way at a time
                     constexpr int kPer = 32 / (D / 8);
@@ -974,7 +1027,8 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             const int s = s0 + u * kPer + lane / (D / 8), y = t0 + s;
-                            put_row<D>(f[u], p.signs, false, 1.f, y >= wk.Lq && y < wk.L ? sk : nullptr, kKeyPitch, slot_of(s, vn), kn);
+                            put_row<D, EXACT>(f[u], p.signs, false, 1.f, y >= wk.Lq && y < wk.L ? sk : nullptr, kLow, kKeyPitch, slot_of(s, vn),
+                                              kn);
                         }
                     }
                 }
@@ -1073,7 +1127,7 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
             // S of the first two tiles, then for each tile: O += P V, S of the tile after the next
 #pragma unroll 1
             for (int j = -2; j < wk.n_tile && ok; ++j) {
-                const int ahead = j + 2, vs = j & (kStages - 1), ks = ahead & (kStages - 1);
+                const int ahead = j + 2, vs = j & (kStages - 1), ks = ahead & (kKeyStages - 1);
                 const uint32_t tile = tmem + (m * 2 + (j & 1)) * kTile;
                 if (j >= 0) {
                     ok = reached(&sm.vfull[vs], (j / kStages) & 1) && reached(&sm.pfull[m][j & 1], (j >> 1) & 1);
@@ -1091,15 +1145,28 @@ __global__ void __launch_bounds__(kThreads, 1) sink_prefill_kernel(const __grid_
                     if (j + kStages < wk.n_tile) commit(&sm.vempty[vs]);
                 }
                 if (ahead >= wk.n_tile) continue;
-                ok = reached(&sm.kfull[ks], (ahead / kStages) & 1);
+                ok = reached(&sm.kfull[ks], (ahead / kKeyStages) & 1);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t k = kd + uint64_t(ks * kKStep);
-                mma_ss<false>(tile, qd, k, kS);
+                const auto product = [&](uint64_t qa, uint64_t kb) {
 #pragma unroll
-                for (int s = 1; s < D / 16; ++s) mma_ss<true>(tile, qd + s * (2 * kQueryPitch >> 4), k + s * (2 * kKeyPitch >> 4), kS);
+                    for (int s = 1; s < D / 16; ++s) mma_ss<true>(tile, qa + s * (2 * kQueryPitch >> 4), kb + s * (2 * kKeyPitch >> 4), kS);
+                };
+                if (EXACT) {                              // the low parts first: their sums are small, and so is what is cut off them
+                    mma_ss<false>(tile, qd, k + (kLow >> 4), kS);
+                    product(qd, k + (kLow >> 4));
+                    if (!a.q_bf16 || p.rotate) {
+                        mma_ss<true>(tile, qd + (kQueryLow >> 4), k, kS);
+                        product(qd + (kQueryLow >> 4), k);
+                    }
+                    mma_ss<true>(tile, qd, k, kS);
+                } else {
+                    mma_ss<false>(tile, qd, k, kS);
+                }
+                product(qd, k);
                 commit(&sm.sfull[m][j & 1]);
-                if (ahead + kStages < wk.n_tile) commit(&sm.kempty[ks]);
+                if (ahead + kKeyStages < wk.n_tile) commit(&sm.kempty[ks]);
             }
         }
     }
@@ -1121,8 +1188,10 @@ cudaError_t launch_d(const Params& p, const Args& a, int sms, unsigned* status, 
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     constexpr int kBytes = int(sizeof(Smem<D>)) + 128;
     if (!opted[dev]) {
-        for (auto* kernel : {sink_prefill_kernel<D, false, false>, sink_prefill_kernel<D, true, false>,
-                             sink_prefill_kernel<D, false, true>, sink_prefill_kernel<D, true, true>}) {
+        for (auto* kernel : {sink_prefill_kernel<D, false, false, false>, sink_prefill_kernel<D, true, false, false>,
+                             sink_prefill_kernel<D, false, true, false>, sink_prefill_kernel<D, true, true, false>,
+                             sink_prefill_kernel<D, false, false, true>, sink_prefill_kernel<D, true, false, true>,
+                             sink_prefill_kernel<D, false, true, true>, sink_prefill_kernel<D, true, true, true>}) {
             const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
             if (e != cudaSuccess) return e;
         }
@@ -1150,8 +1219,10 @@ cudaError_t launch_d(const Params& p, const Args& a, int sms, unsigned* status, 
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = ctas > 1 ? 1 : 0;
-    auto* kernel = a.kpc ? ctas > 1 ? sink_prefill_kernel<D, true, true> : sink_prefill_kernel<D, false, true>
-                   : ctas > 1 ? sink_prefill_kernel<D, true, false> : sink_prefill_kernel<D, false, false>;
+    auto* kernel = !a.cu_q ? a.kpc ? ctas > 1 ? sink_prefill_kernel<D, true, true, true> : sink_prefill_kernel<D, false, true, true>
+                             : ctas > 1 ? sink_prefill_kernel<D, true, false, true> : sink_prefill_kernel<D, false, false, true>
+                   : a.kpc ? ctas > 1 ? sink_prefill_kernel<D, true, true, false> : sink_prefill_kernel<D, false, true, false>
+                           : ctas > 1 ? sink_prefill_kernel<D, true, false, false> : sink_prefill_kernel<D, false, false, false>;
     return cudaLaunchKernelEx(&cfg, kernel, p, a, ctas, status);
 }
 

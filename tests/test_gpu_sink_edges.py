@@ -1,6 +1,6 @@
 """The attention with sinks at its edges, against fp64 numpy over the oracle's cache: clusters whose CTAs have no
-tile, weights far below the largest, value scales far apart, queries with NaN, caches that are
-elsewhere, first calls from several threads."""
+tile, weights far below the largest, value scales far apart, scores of single tokens, queries with
+NaN, caches that are elsewhere, first calls from several threads."""
 import os
 import subprocess
 import sys
@@ -174,6 +174,68 @@ def test_value_groups_of_different_scales(vb, vg, d, large):
            + 2.0 ** (s - 36) * a.max() * (code + np.abs(zero) + c).sum(0))
     ref.check_bf16(out.float().cpu().numpy()[0], want[0], tol=np.broadcast_to(tol, want[0].shape))
     ref.check_lse(lse.cpu().numpy(), want_lse, np.full(want_lse.shape, 2.0 ** -14))
+
+
+
+# ---------------------------------------------------------------- scores of single tokens
+
+SINGLE = {
+    "exact_codes": dict(),
+    "exact_codes_rotated": dict(rotate_keys=True, window=40),
+    "groups16": dict(k_group=16, v_group=32, window=16),
+    "groups16_d64": dict(k_group=16, head_dim=64, v_group=64),
+    "groups16_rotated": dict(k_group=16, rotate_keys=True, window=40),
+    "per_channel": dict(k_per_channel=True, window=16),
+    "per_channel_g16": dict(k_per_channel=True, k_group=16),
+    "per_channel_d64": dict(k_per_channel=True, k_group=64, head_dim=64, v_group=64),
+}
+
+
+@pytest.mark.parametrize("kb", [1, 2, 4, 8])
+@pytest.mark.parametrize("length", [200, 5000])
+@pytest.mark.parametrize("layout", list(SINGLE))
+def test_single_tokens_have_fp32_scores(layout, length, kb):
+    """lse of single tokens where every fp16 rounding would go the same way: keys 1 and 1 + 3*2^-13 (a quarter of their groups
+    the latter), queries 1 + 2^-12 with as much again from channel to channel.  Keys and queries count to 2^-22 of
+    themselves (or half of fp16's smallest step, 2^-25), products are exact, and the fp32 sums of a score have up to 40
+    terms (products of 16 channels, of the two parts, of 32-channel units), each off by up to 2^-23 of the magnitudes'
+    sum:
+        |score error| <= |sm_scale| (sum |q_j k_j| (2^-21 + 40 * 2^-23) + sum |q_j| 2^-25)
+    and lse by as much and its own fp32 steps.  (Rounded to fp16, keys alone would move it by 8e-4.)"""
+    w = small(batch=2, num_kv_heads=2, num_q_heads=6, in_dtype=wl.DT_F32, k_bits=kb, **SINGLE[layout])
+    lens, d, r = np.array([length, 77], np.int32), w.head_dim, np.random.default_rng(11)
+    pair = Pair(w, lens)
+    pair.lens[:] = 0
+    pair.glens.zero_()
+    total = int(lens.sum())
+    k = np.where(r.random((total, 2, d)) < 0.25, 1.0 + 3 * 2.0 ** -13, 1.0).astype(np.float32)
+    v = r.standard_normal((total, 2, d)).astype(np.float32)
+    pair.append(k, v, np.array([0, length, total], np.int32))
+    if w.rotate_keys:                            # (fp32 rotations differ in their last bits: the GPU's codes are the cache)
+        for name in ("k_codes", "k_meta", "v_codes", "v_meta", "k_win", "v_win"):
+            o = getattr(pair.ocache, name).view(np.uint8).ravel()
+            if getattr(pair.gcache, name) is not None:
+                o[:] = pair.gpu_bytes(name)[: o.size]
+    q = (1.0 + 2.0 ** -12 * (1 + np.arange(d) % 2 * 2.0 ** -8) + np.zeros((2, 6, d))).astype(np.float32)
+    scale = d ** -0.5
+    out, lse = kvq.sink_decode_attention(pair.glay, pair.gcache, torch_raw(q), pair.glens, length, 4, 3000)
+    _, want = ref.attention(pair.ocache, pair.pt, pair.signs, q.astype(np.float64), np.ones(2, int), pair.lens, 4, 3000, scale)
+    keys = np.abs(pair.ocache.dequantize(pair.lens, length)[0].astype(np.float64))
+    D = np.zeros((2, 6))
+    for b in range(2):
+        paged = np.arange(lens[b]) < ref.paged_len(pair.olay, lens[b])
+        for h in range(6):
+            x, qh = keys[b, h // 3, : lens[b]], np.abs(q[b, h].astype(np.float64))
+            turned = np.zeros(lens[b])
+            if w.rotate_keys:
+                # codes and zero points are larger than the keys they add up to; a rotated query's channel is off by ten
+                # steps of sums that are at most sum |q| / sqrt(d)
+                x = np.where(paged[:, None], 3 * np.repeat(x.reshape(lens[b], -1, w.k_group).max(-1), w.k_group, -1), x)
+                turned = paged * 10 * 2.0 ** -24 * qh.sum() / np.sqrt(d) * x.sum(-1)
+            rot = np.abs((q[b, h] * pair.signs) @ ref.hadamard(d)) if w.rotate_keys else qh
+            mag = np.where(paged, x @ rot, x @ qh)
+            D[b, h] = scale * (mag * (2.0 ** -21 + 40 * 2.0 ** -23) + np.maximum(rot.sum(), qh.sum()) * 2.0 ** -25 + turned).max()
+    ref.check_lse(lse.cpu().numpy(), want, D + 2.0 ** -21 * (1 + np.abs(want)))
 
 
 # ---------------------------------------------------------------- NaN
