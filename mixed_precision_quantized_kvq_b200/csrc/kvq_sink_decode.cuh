@@ -8,7 +8,12 @@
 // 8 bits, masked out of its word where it sits within the low ten bits of a
 // half-word, IS an fp16 number, c * 2^(position - 24) (a subnormal one, exact).
 // The power of two of its position is divided out of the other operand, 2^24
-// out of the result.  One mask per two codes is all the unpacking there is.
+// out of the result.  One mask per two codes is all the unpacking there is,
+// after a rotation of key words that puts 1- and 2-bit codes (and, where the
+// query has a low part, 4-bit ones) high among the ten bits: sums are
+// aligned to the exponents that the operands' fields name, so each zero above a
+// subnormal's first bit costs them a bit (1-bit codes at bits 0 to 3: scores off
+// by up to 2^-17 of sum |q k|, at bits 6 to 9 by 2^-22).
 //
 // What bounds it: latency.  It has to read the codes and metadata of the
 // visible positions (116 bytes per position and kv-head for 4-bit keys and
@@ -161,9 +166,9 @@ __device__ __forceinline__ int pair_channel(int c, int i, int hi) {
     if (KB == 2) return 16 * (c >> 1) + 4 * (c & 1) + i + 8 * hi;
     return 4 * c + i + 16 * hi;
 }
-template <int KB>
+template <int KB, bool LO>
 __device__ __forceinline__ constexpr int pair_bit(int i) {
-    return KB == 4 ? 4 * (i & 1) : KB == 2 ? 2 * i : KB == 1 ? i : 0;
+    return KB == 4 ? 4 * (i & 1) + (LO ? 2 : 0) : KB == 2 ? (LO ? 6 + 2 * (i & 1) : 2 + 2 * i) : KB == 1 ? 6 + i : 0;
 }
 
 // Shared memory of a CTA: what the query fragments are made of, then the
@@ -308,32 +313,35 @@ __device__ __forceinline__ void page_scores(const Params& p, unsigned char* sk, 
                     x[2] = w1 & 0x00ff00ffu;
                     x[3] = (w1 >> 8) & 0x00ff00ffu;
                 } else if (KB == 4) {
-                    const uint32_t w = lds32(k + u * (kPage * 16) + c * 4), v = w >> 8;
-                    x[0] = w & 0x000f000fu;
-                    x[1] = w & 0x00f000f0u;
-                    x[2] = v & 0x000f000fu;
-                    x[3] = v & 0x00f000f0u;
+                    constexpr int kUp = pair_bit<KB, LO>(0);
+                    const uint32_t word = lds32(k + u * (kPage * 16) + c * 4), w = word << kUp, v = word >> (8 - kUp);
+                    x[0] = w & (0x000f000fu << kUp);
+                    x[1] = w & (0x00f000f0u << kUp);
+                    x[2] = v & (0x000f000fu << kUp);
+                    x[3] = v & (0x00f000f0u << kUp);
                 } else if (KB == 2) {
-                    const uint32_t w = lds32(k + (u >> 1) * (kPage * 16) + (2 * (u & 1) + (c >> 1)) * 4) >> (8 * (c & 1));
-                    x[0] = w & 0x00030003u;
-                    x[1] = w & 0x000c000cu;
-                    x[2] = w & 0x00300030u;
-                    x[3] = w & 0x00c000c0u;
+                    const uint32_t word = lds32(k + (u >> 1) * (kPage * 16) + (2 * (u & 1) + (c >> 1)) * 4);
+                    const uint32_t v = __funnelshift_l(word, word, 2 - 8 * (c & 1));
+                    const uint32_t w = LO ? __funnelshift_l(word, word, 6 - 8 * (c & 1)) : v;
+                    x[0] = w & (0x00030003u << pair_bit<KB, LO>(0));
+                    x[1] = w & (0x00030003u << pair_bit<KB, LO>(1));
+                    x[2] = v & (0x00030003u << pair_bit<KB, LO>(2));
+                    x[3] = v & (0x00030003u << pair_bit<KB, LO>(3));
                 } else {
-                    const uint32_t w = lds32(k + u * 4) >> (4 * c);
-                    x[0] = w & 0x00010001u;
-                    x[1] = w & 0x00020002u;
-                    x[2] = w & 0x00040004u;
-                    x[3] = w & 0x00080008u;
+                    const uint32_t word = lds32(k + u * 4), w = __funnelshift_l(word, word, 6 - 4 * c);
+                    x[0] = w & 0x00400040u;
+                    x[1] = w & 0x00800080u;
+                    x[2] = w & 0x01000100u;
+                    x[3] = w & 0x02000200u;
                 }
             }
             float d[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(d, e[0], f[0], e[1], f[1], qh[4 * u], qh[4 * u + 1]);
-            mma_f16(d, e[2], f[2], e[3], f[3], qh[4 * u + 2], qh[4 * u + 3]);
-            if (LO) {
+            if (LO) {   // first: its sums are small, and so is what the products cut off them
                 mma_f16(d, e[0], f[0], e[1], f[1], ql[LO ? 4 * u : 0], ql[LO ? 4 * u + 1 : 0]);
                 mma_f16(d, e[2], f[2], e[3], f[3], ql[LO ? 4 * u + 2 : 0], ql[LO ? 4 * u + 3 : 0]);
             }
+            mma_f16(d, e[0], f[0], e[1], f[1], qh[4 * u], qh[4 * u + 1]);
+            mma_f16(d, e[2], f[2], e[3], f[3], qh[4 * u + 2], qh[4 * u + 3]);
             const float s0 = low_half(m0[u]), s1 = low_half(m1[u]);
             a[0] = fmaf(s0, d[0], a[0]);
             a[1] = fmaf(s0, d[1], a[1]);
@@ -674,7 +682,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) sink_decode_kernel(const __gri
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int c0 = 32 * u + pair_channel<KB>(c, i, 0), c1 = 32 * u + pair_channel<KB>(c, i, 1);
-            const float down = 1.f / float(1 << pair_bit<KB>(i));
+            const float down = 1.f / float(1 << pair_bit<KB, LO>(i));
             qh[4 * u + i] = half2_bits(__half2float(hd.qh[r][c0]) * down, __half2float(hd.qh[r][c1]) * down);
             if (LO) ql[LO ? 4 * u + i : 0] = half2_bits(__half2float(hd.ql[r][c0]) * down, __half2float(hd.ql[r][c1]) * down);
         }

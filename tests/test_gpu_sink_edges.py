@@ -238,6 +238,39 @@ def test_single_tokens_have_fp32_scores(layout, length, kb):
     ref.check_lse(lse.cpu().numpy(), want, D + 2.0 ** -21 * (1 + np.abs(want)))
 
 
+
+@pytest.mark.parametrize("dtype", [wl.DT_BF16, wl.DT_F32])
+@pytest.mark.parametrize("kb", [1, 2, 4, 8])
+@pytest.mark.parametrize("d,kg", [(64, 32), (64, 64), (128, 32), (128, 128)])
+def test_sums_over_raw_codes(d, kg, kb, dtype):
+    """One position, so that lse is its score: 64 keys that are codes times a scale, eight random queries each.  The
+    products of bf16 queries and codes are exact; an fp32 query's two parts are 2^-22 of it off; the score then has at
+    most 16 sums (four products of a unit of 32 channels, two of them low; four units), each off by 2^-24 of the
+    magnitudes' sum:
+        |error| <= (2^-22 + 2^-20) sum |q_j k_j|, and half a step of the result."""
+    B, r = 64, np.random.default_rng(1)
+    w = small(batch=B, num_kv_heads=1, num_q_heads=8, head_dim=d, k_bits=kb, k_group=kg, v_group=64, in_dtype=wl.DT_F32)
+    pair = Pair(w, np.ones(B, np.int32))
+    pair.lens[:] = 0
+    pair.glens.zero_()
+    code = r.integers(0, 2 ** kb, (B, 1, d // kg, kg)) * 1.0
+    code[..., 0], code[..., 1] = 0, 2 ** kb - 1
+    scale = r.integers(1, 256, (B, 1, d // kg, 1)) / 16.0
+    k = (code * scale).reshape(B, 1, d).astype(np.float32)
+    pair.append(k, np.zeros_like(k), np.arange(B + 1, dtype=np.int32))
+    pair.compare_cache()
+    q = r.standard_normal((B, 8, d)).astype(np.float32)
+    raw = q
+    if dtype == wl.DT_BF16:
+        raw = wl.bf16_bits(q)
+        q = wl.bf16_to_f32(raw)
+    _, lse = kvq.sink_decode_attention(pair.glay, pair.gcache, torch_raw(raw), pair.glens, 1, 0, 1, 1.0)
+    kk = pair.ocache.dequantize(pair.lens, 1)[0][:, 0, 0].astype(np.float64)
+    want = np.einsum("bhd,bd->bh", q.astype(np.float64), kk)
+    ref.check_lse(lse.cpu().numpy(), want, (2.0 ** -22 + 2.0 ** -20) * np.einsum("bhd,bd->bh", np.abs(q), kk)
+                  + 2.0 ** -22 * np.abs(want))
+
+
 # ---------------------------------------------------------------- NaN
 
 @pytest.mark.parametrize("form", ["token", "chunk shared by a cluster", "chunk"])
