@@ -173,12 +173,11 @@ __device__ __forceinline__ constexpr int pair_bit(int i) {
 
 // Shared memory of a CTA: what the query fragments are made of, then the
 // warps' buffers; the partial sums take the buffers' place at the end.
-template <int D>
+template <int D, bool LO>
 struct Head {
     __half qh[kHeads][D];                    // query, scaled to at most 2^8 per head, high and low part
     __half ql[kHeads][D];
-    __nv_bfloat16 bh[kHeads][D + 8];         // unrotated query for the ring, high and low part
-    __nv_bfloat16 bl[kHeads][D + 8];
+    __nv_bfloat16 bq[LO ? 3 : 1][kHeads][D + 8];   // unrotated query for the ring: high part and, of fp32 queries, two low ones
     float qsum[kHeads][4];                   // sums over 32 channels
     float factor[kHeads];                    // score scale * log2(e) / query scaling
 };
@@ -204,9 +203,9 @@ __host__ __device__ int warp_smem(const Params& p) {
     const int both = Buf<D, KB, VB>::keys() + Buf<D, KB, VB>::values(p), part = kPartFloats<D> * 4;
     return both > part ? both : part;
 }
-template <int D, int KB, int VB>
+template <int D, int KB, int VB, bool LO>
 __host__ __device__ int decode_smem(const Params& p, int warps) {
-    return int(sizeof(Head<D>)) + warps * warp_smem<D, KB, VB>(p);
+    return int(sizeof(Head<D, LO>)) + warps * warp_smem<D, KB, VB>(p);
 }
 
 // The running state of a warp: fragments of the output (channels 16*i + r, 16*i + r + 8 of heads 2c, 2c+1; scaled by
@@ -461,26 +460,30 @@ __device__ __forceinline__ int ring_piece(int i, int o) {
 
 // Scores of 16 ring slots whose keys are at `sk`: s[h][e] is slot 8h + r, head 2c + e.  ok: bit i set when slot i holds
 // a visible position (other rows are zeros).
-template <int D>
-__device__ __forceinline__ void ring_scores(const Head<D>& hd, const unsigned char* sk, uint32_t ok, bool lo_part,
+template <int D, bool LO>
+__device__ __forceinline__ void ring_scores(const Head<D, LO>& hd, const unsigned char* sk, uint32_t ok, bool lo_part,
                                             float scale_log2, float (&out)[8][2]) {
     const int lane = threadIdx.x % 32, r = lane >> 2, c = lane & 3;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    // (the low parts' sums of their own: what a product cuts off its sum is as small as the sum)
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, low[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {                   // channels 32*j + 8*c .. + 7 in one 16-byte piece
         const uint4 k0 = lds128(sk + ring_piece<D>(r, 4 * j + c)), k1 = lds128(sk + ring_piece<D>(r + 8, 4 * j + c));
-        const uint4 q = *reinterpret_cast<const uint4*>(&hd.bh[r][32 * j + 8 * c]);
+        const uint4 q = *reinterpret_cast<const uint4*>(&hd.bq[0][r][32 * j + 8 * c]);
         uint32_t a[4] = {k0.x, k1.x, k0.y, k1.y}, b[4] = {k0.z, k1.z, k0.w, k1.w};
         mma_b16(s, a, q.x, q.y);
         mma_b16(s, b, q.z, q.w);
-        if (lo_part) {
-            const uint4 ql = *reinterpret_cast<const uint4*>(&hd.bl[r][32 * j + 8 * c]);
-            mma_b16(s, a, ql.x, ql.y);
-            mma_b16(s, b, ql.z, ql.w);
+        if (LO && lo_part) {
+#pragma unroll
+            for (int part = LO ? 2 : 0; part >= 1; --part) {
+                const uint4 ql = *reinterpret_cast<const uint4*>(&hd.bq[part][r][32 * j + 8 * c]);
+                mma_b16(low, a, ql.x, ql.y);
+                mma_b16(low, b, ql.z, ql.w);
+            }
         }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out[i >> 1][i & 1] = (ok >> (r + 8 * (i >> 1))) & 1u ? s[i] * scale_log2 : -INFINITY;
+    for (int i = 0; i < 4; ++i) out[i >> 1][i & 1] = (ok >> (r + 8 * (i >> 1))) & 1u ? (s[i] + low[i]) * scale_log2 : -INFINITY;
 }
 
 template <int D>
@@ -515,12 +518,12 @@ template <int D, int KB, int VB, bool LO>
 __global__ void __launch_bounds__(kMaxWarps * 32) sink_decode_kernel(const __grid_constant__ Params p, const __grid_constant__ Args a) {
     using G = Buf<D, KB, VB>;
     extern __shared__ __align__(16) unsigned char smem[];
-    Head<D>& hd = *reinterpret_cast<Head<D>*>(smem);
+    Head<D, LO>& hd = *reinterpret_cast<Head<D, LO>*>(smem);
     const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int r = lane >> 2, c = lane & 3;
     const int h = blockIdx.y, b = blockIdx.z, rank = blockIdx.x, ctas = gridDim.x;
     const int region = warp_smem<D, KB, VB>(p);
-    unsigned char* mine = smem + sizeof(Head<D>) + warp * region;
+    unsigned char* mine = smem + sizeof(Head<D, LO>) + warp * region;
     unsigned char *sk = mine, *sv = mine + G::keys();
 
     // A negative score scale becomes the query's sign, so that the largest score is the largest product.
@@ -649,9 +652,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32) sink_decode_kernel(const __gri
         if (x >= kHeads) break;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const __nv_bfloat16 hi = __float2bfloat16_rn(q[y][i]);
-            hd.bh[x][lane * C + i] = hi;
-            hd.bl[x][lane * C + i] = __float2bfloat16_rn(q[y][i] - __bfloat162float(hi));
+            float left = q[y][i];
+#pragma unroll
+            for (int part = 0; part < (LO ? 3 : 1); ++part) {
+                const __nv_bfloat16 b = __float2bfloat16_rn(left);
+                hd.bq[part][x][lane * C + i] = b;
+                left -= __bfloat162float(b);
+                if (a.q_bf16) break;                     // (exact already)
+            }
         }
         if (p.rotate) rotate_warp<D>(q[y], p.signs, lane);
         float m = 0.f, sum = 0.f;
@@ -718,7 +726,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) sink_decode_kernel(const __gri
         if (page)
             page_scores<D, KB, VB, LO>(p, sk, base, ns, lo, Lq, edge, qh, ql, qz, s);
         else if (now >= kIsRing)
-            ring_scores<D>(hd, sk, uint32_t(now), ring_lo, scale_log2, s);
+            ring_scores<D, LO>(hd, sk, uint32_t(now), ring_lo, scale_log2, s);
         __syncwarp();
         copy_keys(k + 1, next);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -755,7 +763,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) sink_decode_kernel(const __gri
 
     // ---- the CTA's sums: weights of its warps' parts, then one part for the CTA in place of warp 0's ----
     __syncthreads();
-    const auto parts = [&](int w) { return reinterpret_cast<float*>(smem + sizeof(Head<D>) + w * region); };
+    const auto parts = [&](int w) { return reinterpret_cast<float*>(smem + sizeof(Head<D, LO>) + w * region); };
     float* weight = reinterpret_cast<float*>(&hd.qh[0][0]);   // [warp][head]; the queries are in registers by now
     if (warp < kHeads / 4) {
         const int x = 4 * warp + r % 4;                       // lanes of one head: c + 4 * (r / 4), warps in steps of 8
@@ -823,10 +831,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32) sink_decode_kernel(const __gri
             for (int i = 0; i < 8; ++i) {
                 const bool have = c0 + i < ctas;
                 const unsigned char* at = cl.map_shared_rank(smem, have ? c0 + i : 0);
-                const Head<D>& other = *reinterpret_cast<const Head<D>*>(at);
+                const Head<D, LO>& other = *reinterpret_cast<const Head<D, LO>*>(at);
                 ref[i] = have ? other.factor[x] : kRefNone;
                 sum[i] = have ? other.qsum[x][0] : 0.f;
-                v[i] = have ? reinterpret_cast<const float2*>(at + sizeof(Head<D>))[e] : make_float2(0.f, 0.f);
+                v[i] = have ? reinterpret_cast<const float2*>(at + sizeof(Head<D, LO>))[e] : make_float2(0.f, 0.f);
             }
             const float before = top;
 #pragma unroll
@@ -853,7 +861,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) sink_decode_kernel(const __gri
 
 // ---------------------------------------------------------------- launch
 
-// CTAs per (sequence, kv-head), at most 16: one sequence of 131072 positions at 8 bits takes 101 us with 16, 144 with 8.
+// CTAs per (sequence, kv-head), at most 16: one sequence of 131072 positions at 8 bits takes 99 us with 16, 144 with 8.
 // A CTA of a round costs about its items (pages or ring pieces, shared by its warps)
 // plus one and a half for its start and its end; the rounds are what `slots` CTAs at a time make of all of them.
 // (64 ragged sequences of 8 kv-heads: 48 us with the 512 CTAs that this gives, 63 with 1536, 100 with 4096; CTAs of two
@@ -908,14 +916,14 @@ cudaError_t launch_decode_one(const Params& p, const Args& a, int sms, cudaStrea
     // four warps a CTA, or as many up to eight as bring the most warps onto an SM (large buffers)
     int warps = 4, per_sm = 1;
     for (int w = 4, most = 0; w <= 8; ++w) {
-        const int n = std::min(kMaxWarps / w, (228 * 1024) / (decode_smem<D, KB, VB>(p, w) + 1024));
+        const int n = std::min(kMaxWarps / w, (228 * 1024) / (decode_smem<D, KB, VB, LO>(p, w) + 1024));
         if (n * w > most) {
             most = n * w;
             warps = w;
             per_sm = n;
         }
     }
-    const int smem = decode_smem<D, KB, VB>(p, warps);
+    const int smem = decode_smem<D, KB, VB, LO>(p, warps);
     const long long bound = std::min<long long>(a.len_cap, (long long)a.sinks + a.span + 2 * kPage);
     const int items = int((bound + kPage - 1) / kPage) + (std::min(p.W, a.len_cap) + kRing - 1) / kRing;
     const int n = split_ctas((long long)p.batch * p.hkv, items, warps, sms * per_sm, most_ctas);

@@ -271,6 +271,26 @@ def test_sums_over_raw_codes(d, kg, kb, dtype):
                   + 2.0 ** -22 * np.abs(want))
 
 
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_fp32_queries_against_the_ring(d):
+    """One position in the ring, so that lse is its score.  Queries whose first two bf16 parts leave the same 0.75 * 2^-16 in
+    every channel; three parts hold all of them.  Keys of one sign; a score has at most 24 sums (three parts of eight
+    products of 16 channels), each off by 2^-24 of it: 2^-19, and half a step of the result."""
+    B, r = 16, np.random.default_rng(2)
+    w = small(batch=B, num_kv_heads=1, num_q_heads=8, head_dim=d, v_group=64, window=64, in_dtype=wl.DT_F32)
+    pair = Pair(w, np.ones(B, np.int32))
+    pair.lens[:] = 0
+    pair.glens.zero_()
+    k = (r.integers(64, 128, (B, 1, d)) / 64.0).astype(np.float32)
+    pair.append(k, np.zeros_like(k), np.arange(B + 1, dtype=np.int32))
+    pair.compare_cache()
+    q = np.full((B, 8, d), 1.0 + 2.0 ** -8 + 0.75 * 2.0 ** -16, np.float32)
+    _, lse = kvq.sink_decode_attention(pair.glay, pair.gcache, torch_raw(q), pair.glens, 1, 0, 1, 1.0)
+    want = np.einsum("bhd,bd->bh", q.astype(np.float64), k[:, 0].astype(np.float64))
+    ref.check_lse(lse.cpu().numpy(), want, (2.0 ** -19 + 2.0 ** -23) * want)
+
+
 # ---------------------------------------------------------------- NaN
 
 @pytest.mark.parametrize("form", ["token", "chunk shared by a cluster", "chunk"])
