@@ -29,7 +29,7 @@
 // each 1024 positions, 56% of the copy rate, up to a span of 16384.  Issue slots
 // are 48% busy and DRAM 29%: 16 warps with a stage each for keys and for values do not
 // cover the latency of a page.  Rotated keys and fp32 queries add a low part
-// of the query, whose fragments make the head_dim-128 builds spill (84 to 124
+// of the query, whose fragments make the head_dim-128 builds spill (76 to 124
 // bytes a thread at 128 registers).
 //
 // Work split: one cluster of 1 to 16 CTAs per (sequence, kv-head); its warps
